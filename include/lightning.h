@@ -70,13 +70,21 @@ typedef enum {
     LA_OP_PREFILL = 0,
     LA_OP_PREFILL_VARLEN = 1,
     LA_OP_DECODE = 2,
-    LA_OP_BACKWARD = 3
+    LA_OP_BACKWARD = 3,
+    LA_OP_SCAN = 4,          /* la_selective_scan */
+    LA_OP_SCAN_BACKWARD = 5, /* la_selective_scan_backward */
+    LA_OP_CONV_BACKWARD = 6, /* la_short_conv_backward */
+    LA_OP_NORM_BACKWARD = 7  /* la_layer_norm_backward */
 } la_op;
 
 /*
  * Bytes of workspace an operation needs (0 for decode). For LA_OP_PREFILL and
  * LA_OP_BACKWARD pass B, H, N, d; for LA_OP_PREFILL_VARLEN pass H, total
- * tokens, d and num_seqs (B is ignored). The size depends only on these
+ * tokens, d and num_seqs (B is ignored). For LA_OP_SCAN and
+ * LA_OP_SCAN_BACKWARD pass B = groups G, H = channels D, total tokens, d =
+ * states per channel n and num_seqs; for LA_OP_CONV_BACKWARD H = channels D,
+ * total tokens, d = taps W and num_seqs; for LA_OP_NORM_BACKWARD H = features
+ * F and N = rows (the others are ignored). The size depends only on these
  * arguments, the input dtype and the current tuning (la_set_tuning), never on
  * data. Returns 0 for invalid arguments.
  */
@@ -270,6 +278,196 @@ LA_API int la_backward(const void* dO, const void* q, const void* k, const void*
                        const float* slopes, void* dq, void* dk, void* dv, int B, int H,
                        long long N, int d, int in_t, int out_t, void* workspace, size_t ws_bytes,
                        la_stream_t stream);
+
+/*
+ * State space layer
+ * -----------------
+ * The recurrence beside lightning attention whose decay depends on the input
+ * and on the channel: a selective scan, the short causal convolution before
+ * it and the layer norm around them. The pages have no counterpart; the
+ * formulas below define the operators. Conventions of these entry points:
+ * - Token tensors are token-major, [tokens][features]. `cu_seqlens` == NULL
+ *   means num_seqs sequences of total / num_seqs tokens each, one after the
+ *   other ([B][N][features]); otherwise sequence s covers the rows
+ *   [cu_seqlens[s], cu_seqlens[s+1]) (device int32 [num_seqs + 1],
+ *   non-decreasing, cu_seqlens[0] = 0, at most total: not checked, but values
+ *   outside [0, total] are clamped, so that no access leaves the tensors).
+ *   Rows behind the last sequence are neither read nor written. A sequence
+ *   may be empty: its final state is its incoming one.
+ * - A tensor that comes with an `ld` has `ld` elements between consecutive
+ *   tokens (ld >= its features; elements of one token are contiguous) and
+ *   needs the alignment of its elements only, so it can be a column slice of
+ *   a wider projection. Every other tensor is dense and 16-byte aligned.
+ * - in_t is the dtype of the token inputs, out_t that of the token outputs
+ *   (the same combinations as elsewhere); weights, states of the scan and
+ *   sums over tokens are fp32.
+ * - total <= LA_MAX_TOKENS, num_seqs * D <= 2^31 - 1.
+ * - Outputs must not overlap inputs, except where stated. The current device
+ *   must be the tensors'.
+ */
+
+/*
+ * Token inputs and weights of the scan. For channel c of group g = c / (D/G),
+ * state m < n and token t of a sequence:
+ *     dt     = softplus(delta[t][c] + delta_bias[c])   (without softplus: the sum itself)
+ *     h_t[m] = exp(dt A[c][m]) h_{t-1}[m] + dt u[t][c] B[t][g][m]
+ *     y[t][c] = ( sum_m C[t][g][m] h_t[m] + D[c] u[t][c] ) * z[t][c] sigmoid(z[t][c])
+ * D and delta_bias may be NULL (0), z may be NULL (no gate).
+ *   u, delta, z  [tokens][D] (ld_u, ld_delta, ld_z), dtype in_t
+ *   B, C         [tokens][G][n] (ld_b, ld_c; n contiguous, then G), dtype in_t
+ *   A            [D][n] fp32, D and delta_bias [D] fp32
+ */
+typedef struct {
+    const void* u;
+    const void* delta;
+    const void* z;
+    const void* B;
+    const void* C;
+    long long ld_u, ld_delta, ld_z, ld_b, ld_c;
+    const float* A;
+    const float* D;
+    const float* delta_bias;
+    int softplus;
+} la_scan_inputs;
+
+/* Most states per channel the scan takes (LA_ERR_UNSUPPORTED above). */
+#define LA_MAX_SCAN_STATES 64
+
+/*
+ * The scan over prompts.
+ *   state_in   in   [num_seqs][D][n] fp32, h before the first token, or NULL for zeros;
+ *                   may be the same array as state_out
+ *   y          out  [total][D], dtype out_t
+ *   state_out  out  [num_seqs][D][n] fp32, h after each sequence's last token; may be NULL
+ *   workspace  at least la_workspace_bytes(LA_OP_SCAN, ...) bytes
+ */
+LA_API int la_selective_scan(const int* cu_seqlens, int num_seqs, const la_scan_inputs* in,
+                             const float* state_in, void* y, float* state_out, long long total,
+                             int D, int G, int n, int in_t, int out_t, void* workspace,
+                             size_t ws_bytes, la_stream_t stream);
+
+/*
+ * The scan of one token for each of B sequences: token b is row b of the
+ * inputs, its state state[b] ([B][D][n] fp32) is advanced in place, and the
+ * output uses the advanced state. No workspace.
+ */
+LA_API int la_selective_scan_step(const la_scan_inputs* in, float* state, void* y, int B, int D,
+                                  int G, int n, int in_t, int out_t, la_stream_t stream);
+
+/*
+ * Gradients of the scan, each [as its input] and dense. With dyz = dy z
+ * sigmoid(z) (dy without a gate) and g_t the gradient of h_t,
+ *     g_t = C_t dyz_t + exp(dt_{t+1} A) g_{t+1}   (after the last token: dstate_out)
+ *     dC_t = sum_c dyz h_t,  dB_t = sum_c dt u g_t  (over the group's channels)
+ *     du = D dyz + dt sum_m g B,  dz = dy (y before the gate) (z sigmoid(z))'
+ *     ddt = sum_m A exp(dt A) h_{t-1} g + u sum_m g B,  ddelta = ddt softplus'(delta + delta_bias)
+ *     dA = sum_t dt exp(dt A) h_{t-1} g,  dD = sum_t dyz u,  ddelta_bias = sum_t ddelta
+ *     dstate_in = exp(dt_0 A) g_0
+ * du, ddelta, dB, dC and dA are required; dz must be given exactly when z is;
+ * dD, ddelta_bias and dstate_in may be NULL. The sums over tokens and
+ * channels run in a fixed order: the same call gives the same bits.
+ */
+typedef struct {
+    void* du;
+    void* ddelta;
+    void* dz;
+    void* dB;
+    void* dC;
+    float* dA;
+    float* dD;
+    float* ddelta_bias;
+    float* dstate_in;
+} la_scan_grads;
+
+/*
+ *   dy          in  [total][D] (ld_dy), dtype in_t
+ *   state_in    in  as in the forward call, or NULL
+ *   dstate_out  in  [num_seqs][D][n] fp32, the gradient of state_out, or NULL for zeros
+ *   out         du, ddelta, dz, dB, dC in dtype out_t
+ *   workspace   at least la_workspace_bytes(LA_OP_SCAN_BACKWARD, ...) bytes
+ */
+LA_API int la_selective_scan_backward(const int* cu_seqlens, int num_seqs,
+                                      const la_scan_inputs* in, const float* state_in,
+                                      const void* dy, long long ld_dy, const float* dstate_out,
+                                      const la_scan_grads* out, long long total, int D, int G,
+                                      int n, int in_t, int out_t, void* workspace,
+                                      size_t ws_bytes, la_stream_t stream);
+
+/*
+ * Short causal convolution of each channel over its last W inputs:
+ *     p_t[c] = bias[c] + sum_{j<W} weight[c][j] x_{t-(W-1)+j}[c],   y = silu ? p sigmoid(p) : p
+ * Inputs before a sequence's first token come from state_in (zeros when NULL).
+ *   x          in   [total][D] (ld_x), dtype in_t
+ *   weight     in   [D][W] fp32, W = 2, 3 or 4; bias [D] fp32 or NULL
+ *   state_in   in   [num_seqs][W-1][D], dtype in_t: the W - 1 inputs before the first
+ *                   token, oldest first; or NULL
+ *   y          out  [total][D], dtype out_t
+ *   state_out  out  [num_seqs][W-1][D], dtype in_t: each sequence's last W - 1 inputs; may
+ *                   be NULL, must not overlap state_in
+ * No workspace.
+ */
+LA_API int la_short_conv(const int* cu_seqlens, int num_seqs, const void* x, long long ld_x,
+                         const float* weight, const float* bias, const void* state_in, void* y,
+                         void* state_out, long long total, int D, int W, int silu, int in_t,
+                         int out_t, la_stream_t stream);
+
+/* The convolution of one token for each of B sequences (row b of x); state
+ * [B][W-1][D] is advanced in place. No workspace. */
+LA_API int la_short_conv_step(const void* x, long long ld_x, const float* weight,
+                              const float* bias, void* state, void* y, int B, int D, int W,
+                              int silu, int in_t, int out_t, la_stream_t stream);
+
+/*
+ * Gradients of the convolution: with q_t = dy_t y'(p_t),
+ *     dx_t = sum_j weight_j q_{t+W-1-j},  dweight_j = sum_t q_t x_{t-(W-1)+j},  dbias = sum_t q_t
+ *   dy          in   [total][D] (ld_dy), dtype in_t
+ *   dstate_out  in   [num_seqs][W-1][D], dtype in_t, the gradient of state_out; or NULL
+ *   dx          out  [total][D], dtype out_t
+ *   dweight     out  [D][W] fp32; dbias [D] fp32 or NULL
+ *   dstate_in   out  [num_seqs][W-1][D], dtype out_t; or NULL
+ *   workspace   at least la_workspace_bytes(LA_OP_CONV_BACKWARD, ...) bytes
+ * The sums over tokens run in a fixed order.
+ */
+LA_API int la_short_conv_backward(const int* cu_seqlens, int num_seqs, const void* dy,
+                                  long long ld_dy, const void* x, long long ld_x,
+                                  const float* weight, const float* bias, const void* state_in,
+                                  const void* dstate_out, void* dx, float* dweight, float* dbias,
+                                  void* dstate_in, long long total, int D, int W, int silu,
+                                  int in_t, int out_t, void* workspace, size_t ws_bytes,
+                                  la_stream_t stream);
+
+/* Most features per row of the layer norm (LA_ERR_UNSUPPORTED above). */
+#define LA_MAX_NORM_FEATURES 16384
+
+/*
+ * Layer norm of each row over its F features:
+ *     mean = sum x / F,  rstd = 1 / sqrt( sum (x - mean)^2 / F + eps ),
+ *     y = (x - mean) rstd weight + bias
+ *   x           in   [rows][F], dtype in_t
+ *   weight      in   [F] fp32; bias [F] fp32 or NULL
+ *   eps         in   >= 0 and finite
+ *   y           out  [rows][F], dtype out_t; may be x when the dtypes are the same
+ *   mean, rstd  out  [rows] fp32, what the backward call takes; both or neither NULL
+ * rows may be 0. No workspace.
+ */
+LA_API int la_layer_norm(const void* x, const float* weight, const float* bias, float eps,
+                         void* y, float* mean, float* rstd, long long rows, int F, int in_t,
+                         int out_t, la_stream_t stream);
+
+/*
+ * Gradients of the layer norm: with v = (x - mean) rstd and e = dy weight,
+ *     dx = rstd (e - mean_f e - v mean_f(e v)),  dweight = sum_rows dy v,  dbias = sum_rows dy
+ *   dy, x       in   [rows][F], dtype in_t
+ *   mean, rstd  in   [rows] fp32 from the forward call
+ *   dx          out  [rows][F], dtype out_t
+ *   dweight     out  [F] fp32; dbias [F] fp32 or NULL
+ *   workspace   at least la_workspace_bytes(LA_OP_NORM_BACKWARD, ...) bytes
+ * The sums over rows run in a fixed order. With no rows dweight and dbias are zeros.
+ */
+LA_API int la_layer_norm_backward(const void* dy, const void* x, const float* weight,
+                                  const float* mean, const float* rstd, void* dx, float* dweight,
+                                  float* dbias, long long rows, int F, int in_t, int out_t,
+                                  void* workspace, size_t ws_bytes, la_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 LA_API const char* la_status_string(int status);

@@ -8,4 +8,7 @@ from .binding import (LA_BF16, LA_F32, LA_OP_BACKWARD, LA_OP_DECODE, LA_OP_PREFI
                       LA_OP_PREFILL_VARLEN, LightningError, backward, decode, la_backward,
                       la_decode, la_get_tuning, la_last_launch_count, la_prefill,
                       la_prefill_varlen, la_read_device_status, la_set_tuning, la_status_string,
-                      la_workspace_bytes, lib, prefill, prefill_varlen, workspace)
+                      la_workspace_bytes, layer_norm, layer_norm_backward, lib, prefill,
+                      prefill_varlen, selective_scan, selective_scan_backward,
+                      selective_scan_step, short_conv, short_conv_backward, short_conv_step,
+                      workspace)

@@ -22,14 +22,32 @@ LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT, LA_E
     0, -1, -2, -3, -4, -5)
 LA_BF16, LA_F32 = 0, 1
 LA_OP_PREFILL, LA_OP_PREFILL_VARLEN, LA_OP_DECODE, LA_OP_BACKWARD = 0, 1, 2, 3
+LA_OP_SCAN, LA_OP_SCAN_BACKWARD, LA_OP_CONV_BACKWARD, LA_OP_NORM_BACKWARD = 4, 5, 6, 7
 
 EXPORTED = ["la_workspace_bytes", "la_prefill", "la_prefill_varlen", "la_decode", "la_backward",
             "la_status_string", "la_read_device_status", "la_set_tuning", "la_get_tuning",
             "la_last_launch_count", "la_prefill_noalloc", "la_set_fault_injection",
             "la_prefill_with_state", "la_prefill_varlen_with_state", "la_mixed_step",
-            "la_output_norm_gate", "la_state_prefix", "la_prefill_state", "la_noalloc_device_status"]
+            "la_output_norm_gate", "la_state_prefix", "la_prefill_state", "la_noalloc_device_status",
+            "la_selective_scan", "la_selective_scan_step", "la_selective_scan_backward",
+            "la_short_conv", "la_short_conv_step", "la_short_conv_backward", "la_layer_norm",
+            "la_layer_norm_backward"]
 
 _lib = None
+
+
+class ScanInputs(ctypes.Structure):
+    """la_scan_inputs of include/lightning.h."""
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("u", "delta", "z", "B", "C")]
+                + [(f, ctypes.c_longlong) for f in ("ld_u", "ld_delta", "ld_z", "ld_b", "ld_c")]
+                + [(f, ctypes.c_void_p) for f in ("A", "D", "delta_bias")]
+                + [("softplus", ctypes.c_int)])
+
+
+class ScanGrads(ctypes.Structure):
+    """la_scan_grads of include/lightning.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("du", "ddelta", "dz", "dB", "dC", "dA", "dD",
+                                               "ddelta_bias", "dstate_in")]
 
 
 class LightningError(RuntimeError):
@@ -60,6 +78,17 @@ def lib():
         L.la_state_prefix.argtypes = [P, P, ctypes.POINTER(LL), I, I, I, I, I, P, P]
         L.la_output_norm_gate.argtypes = [P, P, P, ctypes.c_float, P, I, I, LL, I, I, I, P]
         L.la_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, LL, I, I, I, P, SZ, P]
+        SI, SG = ctypes.POINTER(ScanInputs), ctypes.POINTER(ScanGrads)
+        L.la_selective_scan.argtypes = [P, I, SI, P, P, P, LL, I, I, I, I, I, P, SZ, P]
+        L.la_selective_scan_step.argtypes = [SI, P, P, I, I, I, I, I, I, P]
+        L.la_selective_scan_backward.argtypes = [P, I, SI, P, P, LL, P, SG, LL, I, I, I, I, I, P,
+                                                 SZ, P]
+        L.la_short_conv.argtypes = [P, I, P, LL, P, P, P, P, P, LL, I, I, I, I, I, P]
+        L.la_short_conv_step.argtypes = [P, LL, P, P, P, P, I, I, I, I, I, I, P]
+        L.la_short_conv_backward.argtypes = [P, I, P, LL, P, LL, P, P, P, P, P, P, P, P, LL, I, I,
+                                             I, I, I, P, SZ, P]
+        L.la_layer_norm.argtypes = [P, P, P, ctypes.c_float, P, P, P, LL, I, I, I, P]
+        L.la_layer_norm_backward.argtypes = [P, P, P, P, P, P, P, P, LL, I, I, I, P, SZ, P]
         L.la_status_string.argtypes = [I]
         L.la_status_string.restype = ctypes.c_char_p
         L.la_read_device_status.argtypes = [P, P]
@@ -75,7 +104,9 @@ def lib():
                   "la_decode", "la_backward",
                   "la_read_device_status", "la_set_tuning", "la_get_tuning",
                   "la_last_launch_count", "la_prefill_noalloc", "la_set_fault_injection",
-                  "la_noalloc_device_status"):
+                  "la_noalloc_device_status", "la_selective_scan", "la_selective_scan_step",
+                  "la_selective_scan_backward", "la_short_conv", "la_short_conv_step",
+                  "la_short_conv_backward", "la_layer_norm", "la_layer_norm_backward"):
             getattr(L, f).restype = I
         _lib = L
     return _lib
@@ -280,3 +311,326 @@ def backward(dout, q, k, v, slopes, out_dtype=None, stream=None):
     ws = workspace(LA_OP_BACKWARD, B, H, N, d, 0, q.dtype, q.device)
     la_backward(dout, q, k, v, slopes, dq, dk, dv, ws, stream)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- state space layer
+#
+# Token tensors are [B, N, ...] (num_seqs = B sequences of N tokens) or, with
+# cu_seqlens, [T, ...]; a token input may be a column slice of a wider tensor
+# (any stride between tokens, its last dimensions contiguous).
+
+def _rows(t, lead, inner, what):
+    """Pointer of a token tensor [*lead, *inner] and the elements between its tokens."""
+    k = len(lead)
+    shape, stride = t.shape, t.stride()
+    if shape[:k] != lead or shape[k:] != inner:
+        raise ValueError(f"{what} is {tuple(shape)}, expected {tuple(lead) + tuple(inner)}")
+    dense = 1
+    for n, st in zip(reversed(inner), reversed(stride[k:])):
+        if n != 1 and st != dense:
+            raise ValueError(f"{what}: the elements of a token must be contiguous")
+        dense *= n
+    if k == 1:
+        ld = stride[0] if lead[0] > 1 else dense
+    elif lead[1] > 1:
+        ld = stride[1]
+        if lead[0] > 1 and stride[0] != lead[1] * ld:
+            raise ValueError(f"{what}: the tokens of all sequences must be evenly spaced")
+    else:
+        ld = stride[0] if lead[0] > 1 else dense
+    return (t.data_ptr() if t.numel() else None), ld
+
+
+def _flat(t, shape, dtype, what):
+    """Pointer of a dense tensor of a given shape and dtype; None stays None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr() if t.numel() else None
+
+
+def _same(first, *others):
+    """Every given tensor is on first's device, which is a GPU."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and on {t.device}")
+    return dev
+
+
+def _sequences(x, cu_seqlens, features):
+    """(leading shape, number of sequences, rows, pointer of cu_seqlens)."""
+    if cu_seqlens is None:
+        if x.dim() != 2 + features:
+            raise ValueError(f"expected [B, N, ...] without cu_seqlens, got {tuple(x.shape)}")
+        lead = x.shape[:2]
+        return lead, lead[0], lead[0] * lead[1], None
+    if x.dim() != 1 + features:
+        raise ValueError(f"expected [T, ...] with cu_seqlens, got {tuple(x.shape)}")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+    lead = x.shape[:1]
+    return lead, cu_seqlens.numel() - 1, lead[0], _flat(cu_seqlens, cu_seqlens.shape, torch.int32,
+                                                        "cu_seqlens")
+
+
+class _on:
+    """Makes `stream` (default: the device's current one) current for the allocations of a
+    call and for its launch, on the tensors' device. Inputs that a caller frees while the
+    call runs on another stream than theirs stay allocated until it is done."""
+
+    def __init__(self, dev, stream, inputs):
+        self.guard = None
+        if stream is None:
+            if torch.cuda.current_device() != dev.index:
+                self.guard = torch.cuda.device(dev)
+            stream = torch.cuda.current_stream(dev)
+        else:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            if stream != torch.cuda.current_stream(dev):
+                for t in inputs:
+                    if t is not None:
+                        t.record_stream(stream)
+            self.guard = torch.cuda.stream(stream)  # makes its device current too
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead):
+    """(la_scan_inputs, D, G, n) after checking every shape."""
+    width = u.shape[-1]
+    if A.dim() != 2 or B.dim() != len(lead) + 2:
+        raise ValueError(f"A is [D, n] and B [tokens, G, n], got {tuple(A.shape)}, {tuple(B.shape)}")
+    n, G = A.shape[1], B.shape[-2]
+    for t, what in ((delta, "delta"), (z, "z"), (B, "B"), (C, "C")):
+        if t is not None and t.dtype != u.dtype:
+            raise ValueError(f"{what} is {t.dtype}, u is {u.dtype}")
+    up, ld_u = _rows(u, lead, (width,), "u")
+    dp, ld_d = _rows(delta, lead, (width,), "delta")
+    bp, ld_b = _rows(B, lead, (G, n), "B")
+    cp, ld_c = _rows(C, lead, (G, n), "C")
+    zp, ld_z = (None, 0) if z is None else _rows(z, lead, (width,), "z")
+    f32 = torch.float32
+    s = ScanInputs(up, dp, zp, bp, cp, ld_u, ld_d, ld_z, ld_b, ld_c,
+                   _flat(A, (width, n), f32, "A"), _flat(D, (width,), f32, "D"),
+                   _flat(delta_bias, (width,), f32, "delta_bias"), 1 if softplus else 0)
+    return s, width, G, n
+
+
+def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
+                   state_in=None, cu_seqlens=None, want_state=True, out_dtype=None, stream=None):
+    """Allocate outputs and workspace and run la_selective_scan. u, delta, z
+    [B, N, D] (packed [T, D] with cu_seqlens), A [D, n], B and C [B, N, G, n],
+    D and delta_bias [D], state_in [num_seqs, D, n]. Returns (y, state or None)."""
+    lead, seqs, rows, cu = _sequences(u, cu_seqlens, 1)
+    dev = _same(u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens)
+    s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead)
+    sp = _flat(state_in, (seqs, width, n), torch.float32, "state_in")
+    with _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens)) as handle:
+        y = torch.empty((*lead, width), dtype=out_dtype or u.dtype, device=dev)
+        state = (torch.empty((seqs, width, n), dtype=torch.float32, device=dev)
+                 if want_state else None)
+        need = lib().la_workspace_bytes(LA_OP_SCAN, G, width, rows, n, seqs, _dt(u))
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check("la_selective_scan", lib().la_selective_scan(
+            cu, seqs, s, sp, y.data_ptr() or None, state.data_ptr() or None if want_state else None,
+            rows, width, G, n, _dt(u), _dt(y), ws.data_ptr() if need else None, need, handle))
+    return y, state
+
+
+def selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=None, softplus=True,
+                        out_dtype=None, stream=None):
+    """la_selective_scan_step: one token for each of B sequences (u, delta, z
+    [B, D], B and C [B, G, n]); state [B, D, n] is advanced in place. Returns y [B, D]."""
+    if u.dim() != 2:
+        raise ValueError(f"u is [B, D], got {tuple(u.shape)}")
+    dev = _same(u, delta, A, B, C, D, z, delta_bias, state)
+    s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, u.shape[:1])
+    seqs = u.shape[0]
+    sp = _flat(state, (seqs, width, n), torch.float32, "state")
+    with _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state)) as handle:
+        y = torch.empty((seqs, width), dtype=out_dtype or u.dtype, device=dev)
+        _check("la_selective_scan_step", lib().la_selective_scan_step(
+            s, sp, y.data_ptr() or None, seqs, width, G, n, _dt(u), _dt(y), handle))
+    return y
+
+
+def selective_scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
+                            state_in=None, dstate_out=None, cu_seqlens=None, out_dtype=None,
+                            stream=None):
+    """Gradients of selective_scan for the output gradient dy (and dstate_out,
+    that of the returned state). Returns a dict: du, ddelta, dB, dC, dA, and dz,
+    dD, ddelta_bias, dstate_in where the call has that input."""
+    lead, seqs, rows, cu = _sequences(u, cu_seqlens, 1)
+    dev = _same(u, dy, delta, A, B, C, D, z, delta_bias, state_in, dstate_out, cu_seqlens)
+    s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead)
+    if dy.dtype != u.dtype:
+        raise ValueError(f"dy is {dy.dtype}, u is {u.dtype}")
+    dyp, ld_dy = _rows(dy, lead, (width,), "dy")
+    f32 = torch.float32
+    sp = _flat(state_in, (seqs, width, n), f32, "state_in")
+    dsp = _flat(dstate_out, (seqs, width, n), f32, "dstate_out")
+    with _on(dev, stream, (dy, u, delta, A, B, C, D, z, delta_bias, state_in, dstate_out,
+                           cu_seqlens)) as handle:
+        def new(shape, dtype=f32):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        t = out_dtype or u.dtype
+        out = {"du": new((*lead, width), t), "ddelta": new((*lead, width), t),
+               "dB": new((*lead, G, n), t), "dC": new((*lead, G, n), t), "dA": new((width, n))}
+        if z is not None:
+            out["dz"] = new((*lead, width), t)
+        if D is not None:
+            out["dD"] = new((width,))
+        if delta_bias is not None:
+            out["ddelta_bias"] = new((width,))
+        if state_in is not None:
+            out["dstate_in"] = new((seqs, width, n))
+        g = ScanGrads(*[(out[f].data_ptr() or None) if f in out else None
+                        for f, _ in ScanGrads._fields_])
+        need = lib().la_workspace_bytes(LA_OP_SCAN_BACKWARD, G, width, rows, n, seqs, _dt(u))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check("la_selective_scan_backward", lib().la_selective_scan_backward(
+            cu, seqs, s, sp, dyp, ld_dy, dsp, g, rows, width, G, n, _dt(u), _dt(out["du"]),
+            ws.data_ptr(), ws.numel(), handle))
+    return out
+
+
+def _conv_weights(x, weight, bias):
+    width = x.shape[-1]
+    if weight.dim() != 2:
+        raise ValueError(f"weight is [D, W], got {tuple(weight.shape)}")
+    W = weight.shape[1]
+    return (width, W, _flat(weight, (width, W), torch.float32, "weight"),
+            _flat(bias, (width,), torch.float32, "bias"))
+
+
+def short_conv(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, want_state=True,
+               out_dtype=None, stream=None):
+    """Allocate outputs and run la_short_conv. x [B, N, D] (packed [T, D] with
+    cu_seqlens), weight [D, W], bias [D], state_in [num_seqs, W-1, D] of x's
+    dtype. Returns (y, state or None)."""
+    lead, seqs, rows, cu = _sequences(x, cu_seqlens, 1)
+    dev = _same(x, weight, bias, state_in, cu_seqlens)
+    width, W, wp, bp = _conv_weights(x, weight, bias)
+    xp, ld_x = _rows(x, lead, (width,), "x")
+    sp = _flat(state_in, (seqs, W - 1, width), x.dtype, "state_in")
+    with _on(dev, stream, (x, weight, bias, state_in, cu_seqlens)) as handle:
+        y = torch.empty((*lead, width), dtype=out_dtype or x.dtype, device=dev)
+        state = (torch.empty((seqs, max(W - 1, 0), width), dtype=x.dtype, device=dev)
+                 if want_state else None)
+        _check("la_short_conv", lib().la_short_conv(
+            cu, seqs, xp, ld_x, wp, bp, sp, y.data_ptr() or None,
+            state.data_ptr() or None if want_state else None, rows, width, W, 1 if silu else 0,
+            _dt(x), _dt(y), handle))
+    return y, state
+
+
+def short_conv_step(x, weight, bias, state, silu=True, out_dtype=None, stream=None):
+    """la_short_conv_step: one token for each of B sequences (x [B, D]); state
+    [B, W-1, D] is advanced in place. Returns y [B, D]."""
+    if x.dim() != 2:
+        raise ValueError(f"x is [B, D], got {tuple(x.shape)}")
+    dev = _same(x, weight, bias, state)
+    width, W, wp, bp = _conv_weights(x, weight, bias)
+    seqs = x.shape[0]
+    xp, ld_x = _rows(x, x.shape[:1], (width,), "x")
+    sp = _flat(state, (seqs, W - 1, width), x.dtype, "state")
+    with _on(dev, stream, (x, weight, bias, state)) as handle:
+        y = torch.empty((seqs, width), dtype=out_dtype or x.dtype, device=dev)
+        _check("la_short_conv_step", lib().la_short_conv_step(
+            xp, ld_x, wp, bp, sp, y.data_ptr() or None, seqs, width, W, 1 if silu else 0, _dt(x),
+            _dt(y), handle))
+    return y
+
+
+def short_conv_backward(dy, x, weight, bias=None, silu=True, state_in=None, dstate_out=None,
+                        cu_seqlens=None, out_dtype=None, stream=None):
+    """Gradients of short_conv. Returns a dict: dx, dweight, and dbias,
+    dstate_in where the call has that input."""
+    lead, seqs, rows, cu = _sequences(x, cu_seqlens, 1)
+    dev = _same(x, dy, weight, bias, state_in, dstate_out, cu_seqlens)
+    width, W, wp, bp = _conv_weights(x, weight, bias)
+    if dy.dtype != x.dtype:
+        raise ValueError(f"dy is {dy.dtype}, x is {x.dtype}")
+    xp, ld_x = _rows(x, lead, (width,), "x")
+    dyp, ld_dy = _rows(dy, lead, (width,), "dy")
+    sp = _flat(state_in, (seqs, W - 1, width), x.dtype, "state_in")
+    dsp = _flat(dstate_out, (seqs, W - 1, width), x.dtype, "dstate_out")
+    with _on(dev, stream, (dy, x, weight, bias, state_in, dstate_out, cu_seqlens)) as handle:
+        t = out_dtype or x.dtype
+        out = {"dx": torch.empty((*lead, width), dtype=t, device=dev),
+               "dweight": torch.empty((width, W), dtype=torch.float32, device=dev)}
+        if bias is not None:
+            out["dbias"] = torch.empty((width,), dtype=torch.float32, device=dev)
+        if state_in is not None:
+            out["dstate_in"] = torch.empty((seqs, W - 1, width), dtype=t, device=dev)
+
+        def ptr(f):
+            return (out[f].data_ptr() or None) if f in out else None
+
+        need = lib().la_workspace_bytes(LA_OP_CONV_BACKWARD, 1, width, rows, W, seqs, _dt(x))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check("la_short_conv_backward", lib().la_short_conv_backward(
+            cu, seqs, dyp, ld_dy, xp, ld_x, wp, bp, sp, dsp, ptr("dx"), ptr("dweight"),
+            ptr("dbias"), ptr("dstate_in"), rows, width, W, 1 if silu else 0, _dt(x),
+            _dt(out["dx"]), ws.data_ptr(), ws.numel(), handle))
+    return out
+
+
+def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, stream=None):
+    """la_layer_norm over the last dimension of x (dense). Returns (y, mean,
+    rstd); the last two, fp32 of x's leading shape, are what
+    layer_norm_backward takes (None without want_stats)."""
+    dev = _same(x, weight, bias)
+    F = x.shape[-1]
+    xp = _flat(x, x.shape, x.dtype, "x")
+    wp = _flat(weight, (F,), torch.float32, "weight")
+    bp = _flat(bias, (F,), torch.float32, "bias")
+    rows = x.numel() // F if F else 0
+    with _on(dev, stream, (x, weight, bias)) as handle:
+        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        mean = rstd = None
+        if want_stats:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        _check("la_layer_norm", lib().la_layer_norm(
+            xp, wp, bp, eps, y.data_ptr() or None, mean.data_ptr() or None if want_stats else None,
+            rstd.data_ptr() or None if want_stats else None, rows, F, _dt(x), _dt(y), handle))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, want_bias=True, out_dtype=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias); dbias is None without want_bias."""
+    dev = _same(x, dy, weight, mean, rstd)
+    F = x.shape[-1]
+    f32 = torch.float32
+    xp, dyp = _flat(x, x.shape, x.dtype, "x"), _flat(dy, x.shape, x.dtype, "dy")
+    wp = _flat(weight, (F,), f32, "weight")
+    mp, rp = _flat(mean, x.shape[:-1], f32, "mean"), _flat(rstd, x.shape[:-1], f32, "rstd")
+    rows = x.numel() // F if F else 0
+    with _on(dev, stream, (dy, x, weight, mean, rstd)) as handle:
+        dx = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        dw = torch.empty((F,), dtype=f32, device=dev)
+        db = torch.empty((F,), dtype=f32, device=dev) if want_bias else None
+        need = lib().la_workspace_bytes(LA_OP_NORM_BACKWARD, 1, F, rows, 1, 1, _dt(x))
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check("la_layer_norm_backward", lib().la_layer_norm_backward(
+            dyp, xp, wp, mp, rp, dx.data_ptr() or None, dw.data_ptr() or None,
+            db.data_ptr() or None if want_bias else None, rows, F, _dt(x), _dt(dx), ws.data_ptr(),
+            ws.numel(), handle))
+    return dx, dw, db

@@ -13,8 +13,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblightning.so")
 SOURCES = ["api.cu", "simt_forward.cu", "decode.cu", "tc_forward.cu", "noalloc.cu",
-           "norm_gate.cu", "lasp.cu"]
-HEADERS = ["common.cuh", "kernels.h", "tc_forward.h"]
+           "norm_gate.cu", "lasp.cu", "ssm_api.cu", "ssm_scan.cu", "ssm_scan_backward.cu",
+           "short_conv.cu", "layer_norm.cu"]
+HEADERS = ["common.cuh", "kernels.h", "tc_forward.h", "ssm.h", "ssm_scan.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -37,7 +38,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"),
-           "-o", LIB + ".tmp"]
+           "--threads", "0", "-o", LIB + ".tmp"]
     if verbose:
         cmd += ["-Xptxas", "-v"]
     cmd += [os.path.join(CSRC, f) for f in SOURCES]

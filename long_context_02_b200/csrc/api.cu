@@ -4,12 +4,14 @@
 #include <cstring>
 
 #include "kernels.h"
+#include "ssm.h"
 #include "tc_forward.h"
 
 namespace la {
 
 static thread_local int g_launches = 0;
 void count_launch(int n) { g_launches += n; }
+void reset_launches() { g_launches = 0; }
 
 static int g_block = 0;    // fp32-path tile length, 0 = default
 static int g_segment = 0;  // bf16-path scan segment length, 0 = automatic
@@ -75,8 +77,10 @@ extern "C" {
 LA_API size_t la_workspace_bytes(int op, int B, int H, long long N_or_total, int d, int num_seqs,
                                  int in_t)
 {
-    if (check_d(d) != LA_OK || H <= 0 || N_or_total < 0) return 0;
     if (in_t != LA_BF16 && in_t != LA_F32) return 0;
+    if (op >= LA_OP_SCAN && op <= LA_OP_NORM_BACKWARD)
+        return ssm_workspace_bytes(op, B, H, N_or_total, d, num_seqs);
+    if (check_d(d) != LA_OK || H <= 0 || N_or_total < 0) return 0;
     Problems P;
     P.H = H;
     switch (op) {

@@ -39,5 +39,6 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Launch accounting (per host thread), reported by la_last_launch_count().
 void count_launch(int n = 1);
+void reset_launches();  // every entry point starts with it
 
 }  // namespace la

@@ -1,0 +1,128 @@
+// Device helpers shared by the scan's kernels.
+//
+// Thread layout of every scan kernel: K adjacent lanes hold one channel, each
+// S = 4 of its states (n <= 4 K, the states behind n are zeros: a = 1, B = C
+// = 0), so a CTA of NT threads holds NT / K channels and walks the tokens of
+// one chunk. What depends on (token, channel) alone (the softplus, the gate)
+// is computed once per element by another mapping of the threads, token-major
+// and coalesced, and passed through shared memory.
+#pragma once
+
+#include "ssm.h"
+
+namespace la {
+
+constexpr int SCAN_S = 4;            // states per thread
+constexpr float SCAN_LOG2E = 1.4426950408889634f;
+constexpr float SCAN_LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) <= 1. The logarithm by
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and the series of atanh: its
+// terms are positive, so small results keep their relative precision (the
+// first term left out is below 2^-25 of the sum).
+__device__ __forceinline__ float softplus_f(float x)
+{
+    const float e = __expf(-fabsf(x));
+    const float s = __fdividef(e, 2.f + e), q = s * s;
+    float p = 1.f / 15;
+    p = fmaf(p, q, 1.f / 13);
+    p = fmaf(p, q, 1.f / 11);
+    p = fmaf(p, q, 1.f / 9);
+    p = fmaf(p, q, 1.f / 7);
+    p = fmaf(p, q, 1.f / 5);
+    p = fmaf(p, q, 1.f / 3);
+    p = fmaf(p, q, 1.f);
+    return fmaxf(x, 0.f) + 2.f * s * p;
+}
+
+// Sum V values over the M lanes that differ in the bits [STEP, STEP M) of the
+// lane number. Each step halves the values that a lane keeps, so V values
+// cost about V shuffles instead of V log2 M. On return lane l holds, in v[0
+// .. V/min(V,M) ), the totals with the indices that `reduced_index` names.
+template <int V, int M, int STEP>
+__device__ __forceinline__ void lane_reduce(float* v, int lane)
+{
+    int count = V;
+#pragma unroll
+    for (int m = M / 2; m >= 1; m >>= 1) {
+        const int bit = m * STEP;
+        if (count > 1) {
+            count >>= 1;
+            const bool up = lane & bit;
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if (i < count) {
+                    const float send = up ? v[i] : v[i + count];
+                    const float keep = up ? v[i + count] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+        }
+    }
+}
+// Index of the first value that a lane holds after lane_reduce<V, M, STEP>.
+template <int V, int M, int STEP> __device__ __forceinline__ int reduced_index(int lane)
+{
+    int count = V, at = 0;
+#pragma unroll
+    for (int m = M / 2; m >= 1; m >>= 1) {
+        if (count > 1) {
+            count >>= 1;
+            if (lane & (m * STEP)) at += count;
+        }
+    }
+    return at;
+}
+// Whether a lane is the one that writes (more lanes than values hold copies).
+template <int V, int M, int STEP> __device__ __forceinline__ bool reduced_writer(int lane)
+{
+    return M <= V || (lane & ((M / V - 1) * STEP)) == 0;
+}
+
+// Four states of one channel at p (n of them in all, this thread's start at
+// m0); vectors when a row of n states keeps 16-byte alignment.
+__device__ __forceinline__ void load_states(float* v, const float* p, int m0, int n)
+{
+    if ((n & 3) == 0) {
+        const float4 x = m0 < n ? *reinterpret_cast<const float4*>(p + m0) : make_float4(0, 0, 0, 0);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = m0 + i < n ? p[m0 + i] : 0.f;
+    }
+}
+__device__ __forceinline__ void store_states(float* p, const float* v, int m0, int n)
+{
+    if ((n & 3) == 0) {
+        if (m0 < n) *reinterpret_cast<float4*>(p + m0) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (m0 + i < n) p[m0 + i] = v[i];
+    }
+}
+
+// Lanes per channel for n states.
+inline int scan_lanes(int n) { return n <= 4 ? 1 : n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
+
+#define LA_SCAN_DISPATCH_K(n, CALL)                                                              \
+    switch (scan_lanes(n)) {                                                                     \
+    case 1: CALL(1); break;                                                                      \
+    case 2: CALL(2); break;                                                                      \
+    case 4: CALL(4); break;                                                                      \
+    case 8: CALL(8); break;                                                                      \
+    default: CALL(16); break;                                                                    \
+    }
+
+}  // namespace la
