@@ -41,6 +41,18 @@ template <typename T, int V> __device__ __forceinline__ void store_vec(T* p, con
     }
 }
 
+// V weights from p on; in vectors when V allows.
+template <int V> __device__ __forceinline__ void load_weights(float* v, const float* p)
+{
+    if constexpr (V == 1) {
+        v[0] = __ldg(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(v + i) = __ldg(reinterpret_cast<const float4*>(p + i));
+    }
+}
+
 // Sum over a row's TPR threads, in a fixed order; `red` has a slot per warp.
 template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red)
 {
@@ -97,12 +109,12 @@ __global__ void __launch_bounds__(NT) norm_kernel(const T* x, const float* __res
     for (int m = 0; m < CH; ++m) {
         const int c = (tid + TPR * m) * V;
         if (c < F) {
-            float out[V];
+            float out[V], w[V], b[V];
+            load_weights<V>(w, weight + c);
+            if (bias) load_weights<V>(b, bias + c);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                out[i] = (xs[m].get(i) - mu) * rs * weight[c + i];
-                if (bias) out[i] += bias[c + i];
-            }
+            for (int i = 0; i < V; ++i)
+                out[i] = fmaf((xs[m].get(i) - mu) * rs, w[i], bias ? b[i] : 0.f);
             store_vec<To, V>(y + row * F + c, out);
         }
     }
@@ -145,10 +157,12 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(
         for (int m = 0; m < CH; ++m) {
             const int c = (tid + TPR * m) * V;
             if (c < F) {
+                float w[V];
+                load_weights<V>(w, weight + c);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float v = (xs[m].get(i) - mu) * rs, g = gs[m].get(i);
-                    const float e = g * weight[c + i];
+                    const float e = g * w[i];
                     s1 += e;
                     s2 = fmaf(e, v, s2);
                     dw[m][i] = fmaf(g, v, dw[m][i]);
@@ -164,11 +178,12 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(
         for (int m = 0; m < CH; ++m) {
             const int c = (tid + TPR * m) * V;
             if (c < F) {
-                float out[V];
+                float out[V], w[V];
+                load_weights<V>(w, weight + c);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float v = (xs[m].get(i) - mu) * rs;
-                    out[i] = rs * (gs[m].get(i) * weight[c + i] - m1 - v * m2);
+                    out[i] = rs * (gs[m].get(i) * w[i] - m1 - v * m2);
                 }
                 store_vec<To, V>(dx + row * F + c, out);
             }

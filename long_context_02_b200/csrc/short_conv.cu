@@ -2,21 +2,22 @@
 // and backward (formulas in lightning.h).
 //
 // Streams of 2 (forward) or 3 (backward) values per (token, channel): bound by
-// HBM. A thread owns V adjacent channels (one 16-byte vector where pointers and
+// HBM. A thread owns V = 4 adjacent channels (one vector where pointers and
 // strides allow it, else one channel) and walks a tile of tokens with the last
 // W inputs in registers, so that each input is loaded once; only the W - 1
 // rows before a tile are loaded twice. Tiles cut the packed rows without
 // regard to sequences: at a sequence's first token the window is reloaded from
 // its incoming state.
-#include "ssm.h"
+#include "ssm_scan.cuh"
 
 namespace la {
 namespace {
 
 constexpr int NT = 128;
-constexpr int TILE = 64;       // tokens per thread, forward
-constexpr int BACK_TILE = 64;  // tokens per thread, backward
-constexpr int AHEAD = 8;       // rows loaded before any of them is used
+constexpr int TILE = 64;        // tokens per thread, forward
+constexpr int BACK_TILE = 128;  // tokens per thread, backward
+constexpr int AHEAD = 8;        // rows in flight per thread while the rows before them are used
+constexpr int BACK_AHEAD = 4;   // the same, backward (two rows each)
 
 struct ConvArgs {
     const void* x;
@@ -39,55 +40,101 @@ struct ConvArgs {
     float* db_part;  // [tiles][D]
 };
 
-// V values of type T at p, as stored.
+// V values of type T at p, as stored, read as pairs (a single value is a pair
+// with a zero).
 template <typename T, int V> struct Row {
-    static constexpr int BYTES = V * sizeof(T);
     union {
-        T e[V];
         uint4 q;
         uint2 d;
-        uint32_t w;
+        uint32_t w[4];
+        T one;
     };
     __device__ __forceinline__ Row() {}
     __device__ __forceinline__ void load(const T* p)
     {
-        if (BYTES == 16) q = __ldcs(reinterpret_cast<const uint4*>(p));
-        else e[0] = *p;
+        if constexpr (V == 1) one = *p;
+        else if constexpr (V * sizeof(T) == 16) q = __ldcs(reinterpret_cast<const uint4*>(p));
+        else d = __ldcs(reinterpret_cast<const uint2*>(p));
     }
     __device__ __forceinline__ void zero()
     {
-        if (BYTES == 16) q = make_uint4(0, 0, 0, 0);
-        else e[0] = T(0.f);
+        if constexpr (V == 1) one = T(0.f);
+        else if constexpr (V * sizeof(T) == 16) q = make_uint4(0, 0, 0, 0);
+        else d = make_uint2(0, 0);
     }
     __device__ __forceinline__ void store(T* p) const
     {
-        if (BYTES == 16) __stcs(reinterpret_cast<uint4*>(p), q);
-        else *p = e[0];
+        if constexpr (V == 1) *p = one;
+        else if constexpr (V * sizeof(T) == 16) __stcs(reinterpret_cast<uint4*>(p), q);
+        else __stcs(reinterpret_cast<uint2*>(p), d);
     }
-    __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
-    __device__ __forceinline__ void set(int i, float v) { e[i] = from_f32<T>(v); }
+    __device__ __forceinline__ f2 get(int i) const
+    {
+        if constexpr (V == 1) return pack(to_f32(one), 0.f);
+        else if constexpr (sizeof(T) == 2)
+            return pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else return pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void store_row(T* p, const float* v)
+__device__ __forceinline__ void store_row(T* p, const f2* v)
 {
-    if constexpr (V * sizeof(T) > 16) {  // eight fp32 outputs of eight bf16 inputs
-        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-        __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-    } else {
-        Row<T, V> r;
+    float x[V + 1];
 #pragma unroll
-        for (int i = 0; i < V; ++i) r.set(i, v[i]);
-        r.store(p);
+    for (int i = 0; i < (V + 1) / 2; ++i) unpack(v[i], x[2 * i], x[2 * i + 1]);
+    if constexpr (V == 1) {
+        *p = from_f32<T>(x[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+    } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(x[2], x[3]);
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                       *reinterpret_cast<const uint32_t*>(&hi)));
     }
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// Weights [D][W] and biases of V channels from c on, as pairs of channels.
+template <int W, int V>
+__device__ __forceinline__ void load_weights(const float* weight, const float* bias, int c,
+                                             f2 (*w)[(V + 1) / 2], f2* b)
+{
+    float x[V * W], y[V + 1];
+    if constexpr (V == 1) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) x[j] = weight[(long long)c * W + j];
+        y[0] = bias ? bias[c] : 0.f;
+        y[1] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; i += 4)
+            *reinterpret_cast<float4*>(x + i) =
+                *reinterpret_cast<const float4*>(weight + (long long)c * W + i);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = bias ? bias[c + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            w[j][i] = pack(x[2 * i * W + j], V == 1 ? 0.f : x[((2 * i + 1) % V) * W + j]);
+        b[i] = pack(y[2 * i], y[2 * i + 1]);
+    }
+}
+
+__device__ __forceinline__ f2 sigmoid2(f2 x)
+{
+    float a, b;
+    unpack(add2(ex2_2(mul2(x, pack(-SCAN_LOG2E, -SCAN_LOG2E))), pack(1.f, 1.f)), a, b);
+    return pack(rcp(a), rcp(b));
+}
 
 // CTAs [0, tiles * cblocks) convolve; the CTAs behind them write state_out.
 template <typename T, typename To, int W, int V>
 __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a)
 {
+    constexpr int H = (V + 1) / 2;  // pairs
     const int cb = blockIdx.x % a.cblocks;
     const long long tile = blockIdx.x / a.cblocks;
     const int c = (cb * NT + threadIdx.x) * V;
@@ -109,22 +156,19 @@ __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a)
         }
         return;
     }
-    float w[W][V], b[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = a.weight[(long long)(c + i) * W + j];
-        b[i] = a.bias ? a.bias[c + i] : 0.f;
-    }
+    f2 w[W][H], b[H];
+    load_weights<W, V>(a.weight, a.bias, c, w, b);
     const long long t0 = tile * TILE;
     const long long t1 = t0 + TILE < a.view.total ? t0 + TILE : a.view.total;
     int s = a.view.find(t0);
     if (s >= a.view.num_seqs) return;
-    a.view.range(s, start, end);
 
-    float win[W][V];  // inputs t - (W - 1) .. t
-    // The W - 1 inputs before row t of sequence s.
-    auto fill = [&](long long t) {
+    // The tile's rows, one run per sequence.
+    for (long long t = t0; t < t1; ++s) {
+        if (s >= a.view.num_seqs) return;
+        a.view.range(s, start, end);
+        if (end <= t) continue;
+        f2 win[W][H];  // inputs t - (W - 1) .. t
 #pragma unroll
         for (int j = 1; j < W; ++j) {
             const long long tok = t - W + j;
@@ -133,48 +177,48 @@ __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a)
             else if (st) row.load(st + ((long long)s * (W - 1) + (tok - start + W - 1)) * a.D);
             else row.zero();
 #pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = row.get(i);
+            for (int i = 0; i < H; ++i) win[j][i] = row.get(i);
         }
-    };
-    fill(t0);
-#pragma unroll 1
-    for (long long t = t0; t < t1; t += AHEAD) {
+        const int n = (int)((end < t1 ? end : t1) - t);  // rows of this run
+        const T* xp = x + t * a.ld_x;
+        To* yp = (To*)a.y + t * a.D + c;
         Row<T, V> rows[AHEAD];
+        auto load = [&](int at) {
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            if (t + q < t1) rows[q].load(x + (t + q) * a.ld_x);
-            else rows[q].zero();
-        }
+            for (int q = 0; q < AHEAD; ++q)
+                rows[q].load(xp + (long long)(at + q < n ? at + q : n - 1) * a.ld_x);
+        };
+        load(0);
+#pragma unroll 1
+        for (int at = 0; at < n; at += AHEAD) {
+            Row<T, V> now[AHEAD];
 #pragma unroll
-        for (int q = 0; q < AHEAD; ++q) {
-            const long long tok = t + q;
-            if (tok >= t1) return;
-            if (tok >= end) {  // the next sequence that holds this row
-                do {
-                    if (++s >= a.view.num_seqs) return;
-                    a.view.range(s, start, end);
-                } while (tok >= end);
-                fill(tok);
+            for (int q = 0; q < AHEAD; ++q) now[q] = rows[q];
+            if (at + AHEAD < n) load(at + AHEAD);
+#pragma unroll
+            for (int q = 0; q < AHEAD; ++q) {
+                f2 out[H];
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+                    win[W - 1][i] = now[q].get(i);
+                    f2 p = b[i];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
+                    out[i] = a.silu ? mul2(p, sigmoid2(p)) : p;
+                }
+                if (at + q < n) store_row<To, V>(yp + (long long)(at + q) * a.D, out);
             }
-            float out[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-                win[W - 1][i] = rows[q].get(i);
-                float p = b[i];
-#pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-                out[i] = a.silu ? p * sigmoid(p) : p;
-            }
-            store_row<To, V>((To*)a.y + tok * a.D + c, out);
         }
+        t += n;
     }
 }
 
 template <typename T, typename To, int W, int V>
 __global__ void __launch_bounds__(NT) conv_step_kernel(ConvArgs a)
 {
+    constexpr int H = (V + 1) / 2;
     const int c = (blockIdx.x % a.cblocks * NT + threadIdx.x) * V;
     const long long s = blockIdx.x / a.cblocks;
     if (c >= a.D) return;
@@ -183,14 +227,14 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(ConvArgs a)
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) rows[j].load(st + (long long)j * a.D);
     rows[W - 1].load((const T*)a.x + s * a.ld_x + c);
-    float out[V];
+    f2 w[W][H], b[H], out[H];
+    load_weights<W, V>(a.weight, a.bias, c, w, b);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float p = a.bias ? a.bias[c + i] : 0.f;
+    for (int i = 0; i < H; ++i) {
+        f2 p = b[i];
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            p = fmaf(a.weight[(long long)(c + i) * W + j], rows[j].get(i), p);
-        out[i] = a.silu ? p * sigmoid(p) : p;
+        for (int j = 0; j < W; ++j) p = fma2(w[j][i], rows[j].get(i), p);
+        out[i] = a.silu ? mul2(p, sigmoid2(p)) : p;
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) rows[j + 1].store(st + (long long)j * a.D);
@@ -205,6 +249,7 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(ConvArgs a)
 template <typename T, typename To, int W, int V>
 __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
 {
+    constexpr int H = (V + 1) / 2;
     const int cb = blockIdx.x % a.cblocks;
     const long long tile = blockIdx.x / a.cblocks;
     const int c = (cb * NT + threadIdx.x) * V;
@@ -213,17 +258,18 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
     const T* dy = (const T*)a.dy + c;
     const T* st = a.state_in ? (const T*)a.state_in + c : nullptr;
     const T* dst = a.dstate_out ? (const T*)a.dstate_out + c : nullptr;
-    float w[W][V], b[V], dw[W][V], db[V];
+    const f2 zero = pack(0.f, 0.f), one = pack(1.f, 1.f), minus = pack(-1.f, -1.f);
+    f2 w[W][H], b[H], dw[W][H], db[H];
+    load_weights<W, V>(a.weight, a.bias, c, w, b);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < H; ++i) {
+        db[i] = zero;
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = a.weight[(long long)(c + i) * W + j], dw[j][i] = 0.f;
-        b[i] = a.bias ? a.bias[c + i] : 0.f;
-        db[i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = zero;
     }
     int s;
     long long start, end;
-    float win[W][V], q[W][V];  // inputs t - (W-1) .. t; q_t .. q_{t+W-1}
+    f2 win[W][H], q[W][H];  // inputs t - (W-1) .. t; q_t .. q_{t+W-1}
     // Input row `tok` of sequence s, before its start from the state.
     auto input = [&](long long tok) {
         Row<T, V> row;
@@ -234,36 +280,37 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
         return row;
     };
     // Gradient that state_out sends to input row `tok`.
-    auto from_state = [&](long long tok, float* v) {
+    auto from_state = [&](long long tok, f2* v) {
         const long long r = tok - (end - (W - 1));
         if (!dst || r < 0) return;
         Row<T, V> row;
         row.load(dst + ((long long)s * (W - 1) + r) * a.D);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += row.get(i);
+        for (int i = 0; i < H; ++i) v[i] = add2(v[i], row.get(i));
     };
-    auto pull = [&](float* v) {  // sum_j w_j q_{t + W-1-j}
+    auto pull = [&](f2* v) {  // sum_j w_j q_{t + W-1-j}
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] = 0.f;
+        for (int i = 0; i < H; ++i) {
+            v[i] = mul2(w[0][i], q[W - 1][i]);
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[i] = fmaf(w[j][i], q[W - 1 - j][i], v[i]);
+            for (int j = 1; j < W; ++j) v[i] = fma2(w[j][i], q[W - 1 - j][i], v[i]);
         }
     };
     // One row: window and q move down to row t, whose oldest input and dy are given.
     auto step = [&](const Row<T, V>& oldest, const Row<T, V>& grad) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+        for (int i = 0; i < H; ++i) {
 #pragma unroll
             for (int j = W - 1; j > 0; --j) win[j][i] = win[j - 1][i], q[j][i] = q[j - 1][i];
             win[0][i] = oldest.get(i);
-            float g = grad.get(i);
+            f2 g = grad.get(i);
             if (a.silu) {
-                float p = b[i];
+                f2 p = b[i];
 #pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-                const float sg = sigmoid(p);
-                g *= sg * fmaf(p, 1.f - sg, 1.f);
+                for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
+                // y'(p) = sg (1 + p (1 - sg))
+                const f2 sg = sigmoid2(p);
+                g = mul2(g, mul2(sg, fma2(p, fma2(sg, minus, one), one)));
             }
             q[0][i] = g;
         }
@@ -274,12 +321,12 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
         for (int j = 0; j < W - 1; ++j) {
             const Row<T, V> row = input(last - (W - 2) + j);
 #pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = row.get(i);
+            for (int i = 0; i < H; ++i) win[j][i] = row.get(i);
         }
 #pragma unroll
         for (int j = 0; j < W; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) q[j][i] = 0.f;
+            for (int i = 0; i < H; ++i) q[j][i] = zero;
     };
 
     if (tile >= a.tiles) {
@@ -294,15 +341,13 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
             step(input(t - (W - 1)), g);
         }
         for (; t >= start - (W - 1); --t) {
-            Row<T, V> g;
-            g.zero();
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < H; ++i) {
 #pragma unroll
                 for (int j = W - 1; j > 0; --j) q[j][i] = q[j - 1][i];
-                q[0][i] = 0.f;
+                q[0][i] = zero;
             }
-            float v[V];
+            f2 v[H];
             pull(v);
             from_state(t, v);
             store_row<To, V>((To*)a.dstate_in +
@@ -321,76 +366,97 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
         if (end < t1) t1 = end;
         if (t1 > t0) s = a.view.find(t1 - 1);
     }
-    if (t1 > t0 && s < a.view.num_seqs) {
+    // The tile's rows, one run per sequence, each from its last row down.
+    for (long long t = t1 - 1; t >= t0; --s) {
+        if (s < 0 || s >= a.view.num_seqs) break;
         a.view.range(s, start, end);
+        if (start > t || end == start) continue;
         // rows after the tile in the same sequence
-        long long t = t1 - 1 + (W - 1) < end - 1 ? t1 - 1 + (W - 1) : end - 1;
-        open(t);
-        for (; t >= t1; --t) {
+        long long after = t + (W - 1) < end - 1 ? t + (W - 1) : end - 1;
+        open(after);
+        for (; after > t; --after) {
             Row<T, V> g;
-            g.load(dy + t * a.ld_dy);
-            step(input(t - (W - 1)), g);
+            g.load(dy + after * a.ld_dy);
+            step(input(after - (W - 1)), g);
         }
-#pragma unroll 1
-        for (; t >= t0;) {
-            if (t < start) {  // an earlier sequence's last row
-                do {
-                    if (--s < 0) break;
-                    a.view.range(s, start, end);
-                } while (t < start || end == start);
-                if (s < 0) break;
-                open(t);
+        const long long low = start > t0 ? start : t0;
+        const int n = (int)(t - low + 1);
+        Row<T, V> xs[BACK_AHEAD], gs[BACK_AHEAD];
+        auto load = [&](int at) {
+#pragma unroll
+            for (int k = 0; k < BACK_AHEAD; ++k) {
+                const long long tok = t - (at + k < n ? at + k : n - 1);
+                xs[k] = input(tok - (W - 1));
+                gs[k].load(dy + tok * a.ld_dy);
             }
-            const long long low = start > t0 ? start : t0;
-            long long n = t - low + 1;
-            if (n > AHEAD / 2) n = AHEAD / 2;
-            Row<T, V> xs[AHEAD / 2], gs[AHEAD / 2];
+        };
+        load(0);
+#pragma unroll 1
+        for (int at = 0; at < n; at += BACK_AHEAD) {
+            Row<T, V> xn[BACK_AHEAD], gn[BACK_AHEAD];
 #pragma unroll
-            for (int k = 0; k < AHEAD / 2; ++k)
-                if (k < n) {
-                    xs[k] = input(t - k - (W - 1));
-                    gs[k].load(dy + (t - k) * a.ld_dy);
-                }
+            for (int k = 0; k < BACK_AHEAD; ++k) xn[k] = xs[k], gn[k] = gs[k];
+            if (at + BACK_AHEAD < n) load(at + BACK_AHEAD);
 #pragma unroll
-            for (int k = 0; k < AHEAD / 2; ++k)
-                if (k < n) {
-                    step(xs[k], gs[k]);
-                    float v[V];
+            for (int k = 0; k < BACK_AHEAD; ++k) {
+                if (at + k < n) {
+                    const long long tok = t - at - k;
+                    step(xn[k], gn[k]);
+                    f2 v[H];
                     pull(v);
-                    from_state(t - k, v);
-                    store_row<To, V>((To*)a.dx + (t - k) * a.D + c, v);
+                    if (tok >= end - (W - 1)) from_state(tok, v);
+                    store_row<To, V>((To*)a.dx + tok * a.D + c, v);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
+                    for (int i = 0; i < H; ++i) {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][i] = fmaf(q[0][i], win[j][i], dw[j][i]);
-                        db[i] += q[0][i];
+                        for (int j = 0; j < W; ++j) dw[j][i] = fma2(q[0][i], win[j][i], dw[j][i]);
+                        db[i] = add2(db[i], q[0][i]);
                     }
                 }
-            t -= n;
+            }
         }
+        t -= n;
     }
+    float out[2 * H][W], ob[2 * H];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < H; ++i) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) a.dw_part[(tile * a.D + c + i) * W + j] = dw[j][i];
-        a.db_part[tile * a.D + c + i] = db[i];
+        for (int j = 0; j < W; ++j) unpack(dw[j][i], out[2 * i][j], out[2 * i + 1][j]);
+        unpack(db[i], ob[2 * i], ob[2 * i + 1]);
+    }
+    float* dwp = a.dw_part + (tile * a.D + c) * W;
+    float* dbp = a.db_part + tile * a.D + c;
+    if constexpr (V == 1) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) dwp[j] = out[0][j];
+        dbp[0] = ob[0];
+    } else {
+        const float* flat = &out[0][0];
+#pragma unroll
+        for (int i = 0; i < V * W; i += 4)
+            *reinterpret_cast<float4*>(dwp + i) =
+                make_float4(flat[i], flat[i + 1], flat[i + 2], flat[i + 3]);
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(dbp + i) = make_float4(ob[i], ob[i + 1], ob[i + 2], ob[i + 3]);
     }
 }
 
-bool vec16(const void* p, long long ld, size_t e)
+// Whether every row of p starts on a vector of four elements.
+bool on_vectors(const void* p, long long ld, size_t e)
 {
-    return ((uintptr_t)p & 15) == 0 && (ld * e & 15) == 0;
+    return (uintptr_t)p % (4 * e) == 0 && ld % 4 == 0;
 }
 
-// Calls F<T, To, W, V>: V channels per thread, a 16-byte vector of the inputs
-// when every row of every tensor starts on one, else 1.
-#define LA_CONV_CASE(F, T, To, W, VEC)                                                           \
-    if (vec) F(T, To, W, VEC);                                                                   \
+// Calls F<T, To, W, V>: V = 4 channels per thread when every row of every
+// tensor starts on a vector of four, else 1.
+#define LA_CONV_CASE(F, T, To, W)                                                                \
+    if (vec) F(T, To, W, 4);                                                                     \
     else F(T, To, W, 1)
 #define LA_CONV_TYPES(F, W)                                                                      \
-    if (p.in_t == LA_F32) { LA_CONV_CASE(F, float, float, W, 4); }                               \
-    else if (p.out_t == LA_F32) { LA_CONV_CASE(F, __nv_bfloat16, float, W, 8); }                 \
-    else { LA_CONV_CASE(F, __nv_bfloat16, __nv_bfloat16, W, 8); }
+    if (p.in_t == LA_F32) { LA_CONV_CASE(F, float, float, W); }                               \
+    else if (p.out_t == LA_F32) { LA_CONV_CASE(F, __nv_bfloat16, float, W); }                 \
+    else { LA_CONV_CASE(F, __nv_bfloat16, __nv_bfloat16, W); }
 #define LA_CONV_DISPATCH(F)                                                                      \
     if (p.W == 2) { LA_CONV_TYPES(F, 2) }                                                        \
     else if (p.W == 3) { LA_CONV_TYPES(F, 3) }                                                   \
@@ -406,15 +472,14 @@ ConvArgs base_args(const ConvProblem& p, bool vec)
     a.view = p.view;
     a.D = p.D;
     a.silu = p.silu;
-    const int V = vec ? (p.in_t == LA_BF16 ? 8 : 4) : 1;
+    const int V = vec ? 4 : 1;
     a.cblocks = (p.D + NT * V - 1) / (NT * V);
     return a;
 }
 
 bool use_vectors(const ConvProblem& p)
 {
-    const size_t e = p.in_t == LA_BF16 ? 2 : 4;
-    return (p.D * e & 15) == 0 && vec16(p.x, p.ld_x, e);
+    return p.D % 4 == 0 && on_vectors(p.x, p.ld_x, p.in_t == LA_BF16 ? 2 : 4);
 }
 
 }  // namespace
@@ -463,7 +528,7 @@ cudaError_t launch_short_conv_backward(const ConvProblem& p, const void* dy, lon
                                        float* dweight, float* dbias, void* dstate_in, void* ws,
                                        cudaStream_t stream)
 {
-    const bool vec = use_vectors(p) && vec16(dy, ld_dy, p.in_t == LA_BF16 ? 2 : 4);
+    const bool vec = use_vectors(p) && on_vectors(dy, ld_dy, p.in_t == LA_BF16 ? 2 : 4);
     ConvArgs a = base_args(p, vec);
     a.state_in = state_in;
     a.dy = dy;

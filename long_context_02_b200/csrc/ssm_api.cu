@@ -65,6 +65,10 @@ int check_scan(const la_scan_inputs* in, long long rows, int D, int G, int n, in
         !aligned(in->C, e) || !aligned16(in->A) || !aligned16(in->D) || !aligned16(in->delta_bias))
         return LA_ERR_INVALID_ARG;
     const long long bc = (long long)G * n;
+    if (rows > 1 && (in->ld_u > LA_MAX_LD || in->ld_delta > LA_MAX_LD ||
+                     (in->z && in->ld_z > LA_MAX_LD) || in->ld_b > LA_MAX_LD ||
+                     in->ld_c > LA_MAX_LD))
+        return LA_ERR_UNSUPPORTED;
     if (rows > 1 && (in->ld_u < D || in->ld_delta < D || (in->z && in->ld_z < D) ||
                      in->ld_b < bc || in->ld_c < bc))
         return LA_ERR_INVALID_ARG;
@@ -85,6 +89,7 @@ int check_conv(const void* x, long long ld_x, const float* weight, const float* 
     if (!weight || (rows > 0 && !x)) return LA_ERR_INVALID_ARG;
     if (!aligned(x, elem(in_t)) || !aligned16(weight) || !aligned16(bias))
         return LA_ERR_INVALID_ARG;
+    if (rows > 1 && ld_x > LA_MAX_LD) return LA_ERR_UNSUPPORTED;
     return rows > 1 && ld_x < D ? LA_ERR_INVALID_ARG : LA_OK;
 }
 
@@ -154,6 +159,7 @@ LA_API int la_selective_scan_backward(const int* cu_seqlens, int num_seqs,
         return LA_ERR_INVALID_ARG;
     if (total > 0 && !in->z != !out->dz) return LA_ERR_INVALID_ARG;
     if (!aligned(dy, elem(in_t)) || (total > 1 && ld_dy < D)) return LA_ERR_INVALID_ARG;
+    if (total > 1 && ld_dy > LA_MAX_LD) return LA_ERR_UNSUPPORTED;
     if (!aligned16(state_in) || !aligned16(dstate_out) || !aligned16(out->du) ||
         !aligned16(out->ddelta) || !aligned16(out->dz) || !aligned16(out->dB) ||
         !aligned16(out->dC) || !aligned16(out->dA) || !aligned16(out->dD) ||
@@ -236,6 +242,7 @@ LA_API int la_short_conv_backward(const int* cu_seqlens, int num_seqs, const voi
         return st;
     if (!dweight || (total > 0 && (!dy || !dx))) return LA_ERR_INVALID_ARG;
     if (!aligned(dy, elem(in_t)) || (total > 1 && ld_dy < D)) return LA_ERR_INVALID_ARG;
+    if (total > 1 && ld_dy > LA_MAX_LD) return LA_ERR_UNSUPPORTED;
     if (!aligned16(state_in) || !aligned16(dstate_out) || !aligned16(dx) || !aligned16(dweight) ||
         !aligned16(dbias) || !aligned16(dstate_in))
         return LA_ERR_INVALID_ARG;

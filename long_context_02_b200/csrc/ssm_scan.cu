@@ -34,24 +34,63 @@ struct ScanArgs {
     float* local;   // [items][D][n], chunked only
     float* dtsum;   // [items][D]
     int D, G, n, cpg;  // cpg: channel blocks per group
-    int out_f32;
+    int out_f32, vec;
+};
+
+// Two adjacent channels of a token as loaded: one access where `vec` (every
+// row of every tensor then starts on such a pair), else two.
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const char* base, uint32_t at, uint32_t next, bool vec)
+    {
+        if (vec) w = *reinterpret_cast<const uint32_t*>(base + at);
+        else w = *reinterpret_cast<const uint16_t*>(base + at) |
+                 (uint32_t) * reinterpret_cast<const uint16_t*>(base + at + next) << 16;
+    }
+    __device__ __forceinline__ float lo() const { return __uint_as_float(w << 16); }
+    __device__ __forceinline__ float hi() const { return __uint_as_float(w & 0xffff0000u); }
+};
+template <> struct Pair<float> {
+    float x, y;
+    __device__ __forceinline__ void load(const char* base, uint32_t at, uint32_t next, bool vec)
+    {
+        if (vec) {
+            const float2 v = *reinterpret_cast<const float2*>(base + at);
+            x = v.x, y = v.y;
+        } else {
+            x = *reinterpret_cast<const float*>(base + at);
+            y = *reinterpret_cast<const float*>(base + at + next);
+        }
+    }
+    __device__ __forceinline__ float lo() const { return x; }
+    __device__ __forceinline__ float hi() const { return y; }
 };
 
 // MODE 0: with outputs. MODE 1: the chunks' states only.
+//
+// Per tile of TT tokens: each thread turns E pairs of channels into (dt, dt u),
+// each twice in a row as the packed multiplies want them; then every thread
+// scans its four states of one channel over the tile and leaves its share of
+// C . h in shared memory; then the pairs' threads add the K shares, the skip
+// and the gate and store. The next tile's inputs are loaded into registers
+// before the scan, which hides them.
 template <typename T, int K, int MODE>
-__global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
+__global__ void __launch_bounds__(NT, 4) scan_kernel(ScanArgs a)
 {
     constexpr int S = SCAN_S, NP = S * K, CC = NT / K;
-    constexpr int TT = K == 1 ? 8 : K == 2 || K == 16 ? 16 : 32;  // tokens per tile
-    constexpr int E = TT * CC / NT;                               // elements per thread
-    constexpr int EB = (TT * NP + NT - 1) / NT;
-    constexpr int YS = CC + 32 / K;  // padded row of the output tile
-    constexpr int R = K < 8 ? 8 / K : 1;
-    __shared__ float2 dtu[TT][CC];
-    __shared__ __align__(16) float bc[2][TT][NP];
-    __shared__ float ys[MODE == 0 ? TT : 1][YS];
+    constexpr int TT = K == 1 ? 8 : K == 2 ? 16 : 32;  // tokens per tile
+    constexpr int RP = 2 * K;                          // rows between a thread's pairs
+    constexpr int E = TT / RP;                         // pairs per thread
+    constexpr int RB = NT / NP, EB = (TT + RB - 1) / RB;
+    constexpr uint32_t TS = sizeof(T);
+    extern __shared__ __align__(16) unsigned char smem[];
+    ulonglong2(*dtu)[CC] = reinterpret_cast<ulonglong2(*)[CC]>(smem);  // [TT][CC]
+    float(*bs)[NP] = reinterpret_cast<float(*)[NP]>(dtu + TT);         // [TT][NP]
+    float(*cs)[NP] = bs + TT;
+    float(*ys)[NT] = reinterpret_cast<float(*)[NT]>(cs + TT);          // [TT][NT]
 
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int blocks = a.G * a.cpg;
     const int item = blockIdx.x / blocks, cb = blockIdx.x % blocks;
     const int s = a.ch.seq(item);
@@ -68,19 +107,17 @@ __global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
     // scan mapping
     const int sch = tid / K, m0 = (tid % K) * S, sc = c0 + sch;
     const bool sc_ok = sc < c_end;
-    // element mapping
-    const int ech = tid % CC, etok = tid / CC, ec = c0 + ech;
-    const bool ec_ok = ec < c_end;
+    // pair mapping; channels behind the group's last read the last ones
+    const int pr = tid % (CC / 2), prow = tid / (CC / 2);
+    const int ec = c0 + 2 * pr;
+    const bool lo_ok = ec < c_end, hi_ok = ec + 1 < c_end;
+    const int ch = lo_ok ? 2 * pr : c_end - c0 - (a.vec ? 2 : 1);
+    const uint32_t ch_at = (uint32_t)ch * TS, next = hi_ok ? TS : 0;
 
-    float A2[S], h[S] = {0.f, 0.f, 0.f, 0.f};
-    if (sc_ok) {
-        load_states(A2, a.in.A + (long long)sc * a.n, m0, a.n);
-#pragma unroll
-        for (int i = 0; i < S; ++i) A2[i] *= SCAN_LOG2E;
-    } else {
-#pragma unroll
-        for (int i = 0; i < S; ++i) A2[i] = 0.f;
-    }
+    float A2[S] = {0.f, 0.f, 0.f, 0.f}, h[S] = {0.f, 0.f, 0.f, 0.f};
+    if (sc_ok) load_states(A2, a.in.A + (long long)sc * a.n, m0, a.n);
+    const f2 log2e = pack(SCAN_LOG2E, SCAN_LOG2E);
+    const f2 A01 = mul2(pack(A2[0], A2[1]), log2e), A23 = mul2(pack(A2[2], A2[3]), log2e);
     const long long slot = ((long long)item * a.D + sc) * a.n;
     if (sc_ok) {
         if (MODE == 1) {
@@ -99,115 +136,174 @@ __global__ void __launch_bounds__(NT) scan_kernel(ScanArgs a)
             load_states(h, a.local + first * a.n, m0, a.n);
 #pragma unroll 4
             for (int c = 1; c < chunk; ++c) {
-                float l[S];
+                float l[S], e[S];
                 load_states(l, a.local + (first + (long long)c * a.D) * a.n, m0, a.n);
                 const float d = a.dtsum[first + (long long)c * a.D];
+                unpack(ex2_2(mul2(pack(d, d), A01)), e[0], e[1]);
+                unpack(ex2_2(mul2(pack(d, d), A23)), e[2], e[3]);
 #pragma unroll
-                for (int i = 0; i < S; ++i) h[i] = fmaf(ex2(d * A2[i]), h[i], l[i]);
+                for (int i = 0; i < S; ++i) h[i] = fmaf(e[i], h[i], l[i]);
             }
         }
     }
     if (MODE == 1 && last) return;
+    f2 h01 = pack(h[0], h[1]), h23 = pack(h[2], h[3]);
 
-    const T* up = (const T*)a.in.u + ec;
-    const T* dp = (const T*)a.in.delta + ec;
-    const T* zp = a.in.z ? (const T*)a.in.z + ec : nullptr;
-    const T* Bp = (const T*)a.in.B + (long long)g * a.n;
-    const T* Cp = (const T*)a.in.C + (long long)g * a.n;
-    const float dbias = a.in.delta_bias && ec_ok ? a.in.delta_bias[ec] : 0.f;
-    const float Dw = a.in.D && ec_ok ? a.in.D[ec] : 0.f;
+    const uint32_t lu = (uint32_t)a.in.ld_u * TS, ld = (uint32_t)a.in.ld_delta * TS;
+    const uint32_t lz = (uint32_t)a.in.ld_z * TS;
+    const uint32_t lb = (uint32_t)a.in.ld_b * TS, lc = (uint32_t)a.in.ld_c * TS;
+    const char* up = (const char*)a.in.u + ((long long)c0 + t0 * a.in.ld_u) * TS;
+    const char* dp = (const char*)a.in.delta + ((long long)c0 + t0 * a.in.ld_delta) * TS;
+    const char* zp = (const char*)a.in.z + ((long long)c0 + t0 * a.in.ld_z) * TS;
+    const char* Bp = (const char*)a.in.B + ((long long)g * a.n + t0 * a.in.ld_b) * TS;
+    const char* Cp = (const char*)a.in.C + ((long long)g * a.n + t0 * a.in.ld_c) * TS;
+    const bool gated = a.in.z != nullptr, vec = a.vec;
+    const int bm = tid % NP, brow = tid / NP;
+    const bool bm_ok = bm < a.n;
+    const uint32_t bm_at = (uint32_t)(bm_ok ? bm : 0) * TS;
+    float bias[2] = {0.f, 0.f}, Dw[2] = {0.f, 0.f};
+    if (a.in.delta_bias) {
+        if (lo_ok) bias[0] = a.in.delta_bias[ec];
+        if (hi_ok) bias[1] = a.in.delta_bias[ec + 1];
+    }
+    if (MODE == 0 && a.in.D) {
+        if (lo_ok) Dw[0] = a.in.D[ec];
+        if (hi_ok) Dw[1] = a.in.D[ec + 1];
+    }
 
-    T ru[E], rd[E], rz[E], rB[EB], rC[EB];
-    auto load = [&](long long t) {
+    Pair<T> ru[E], rd[E], rz[E];
+    T rB[EB], rC[EB];
+    auto load = [&](int rmax) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const long long tok = t + e * K + etok;
-            const bool ok = ec_ok && tok < t1;
-            ru[e] = ok ? up[tok * a.in.ld_u] : T(0.f);
-            rd[e] = ok ? dp[tok * a.in.ld_delta] : T(0.f);
-            if (MODE == 0) rz[e] = ok && zp ? zp[tok * a.in.ld_z] : T(0.f);
+            const uint32_t row = min(prow + e * RP, rmax);
+            ru[e].load(up, row * lu + ch_at, next, vec);
+            rd[e].load(dp, row * ld + ch_at, next, vec);
+            if (MODE == 0 && gated) rz[e].load(zp, row * lz + ch_at, next, vec);
         }
 #pragma unroll
         for (int e = 0; e < EB; ++e) {
-            const int idx = e * NT + tid, m = idx % NP;
-            const long long tok = t + idx / NP;
-            const bool ok = m < a.n && tok < t1 && idx < TT * NP;
-            rB[e] = ok ? Bp[tok * a.in.ld_b + m] : T(0.f);
-            if (MODE == 0) rC[e] = ok ? Cp[tok * a.in.ld_c + m] : T(0.f);
+            const uint32_t row = min(brow + e * RB, rmax);
+            rB[e] = *reinterpret_cast<const T*>(Bp + (row * lb + bm_at));
+            if (MODE == 0) rC[e] = *reinterpret_cast<const T*>(Cp + (row * lc + bm_at));
         }
+        up += (long long)TT * lu;
+        dp += (long long)TT * ld;
+        zp += (long long)TT * lz;
+        Bp += (long long)TT * lb;
+        Cp += (long long)TT * lc;
     };
 
     float dts = 0.f;
-    if (t0 < t1) load(t0);
+    // Rows of a tile are counted from its first; rmax is the last that exists.
+    int rmax = (int)(t1 - t0 < TT ? t1 - t0 : TT) - 1;
+    if (t0 < t1) load(rmax);
     for (long long t = t0; t < t1; t += TT) {
-        float cu[E], cz[E];
+        Pair<T> cu[E], cz[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            cu[e] = to_f32(ru[e]);
-            if (MODE == 0) cz[e] = to_f32(rz[e]);
-            float dt = to_f32(rd[e]) + dbias;
-            if (a.in.softplus) dt = softplus_f(dt);
-            if (!ec_ok || t + e * K + etok >= t1) dt = 0.f;
-            dtu[e * K + etok][ech] = make_float2(dt, dt * cu[e]);
+            cu[e] = ru[e];
+            if (MODE == 0) cz[e] = rz[e];
+            const int row = prow + e * RP;
+            float x = rd[e].lo() + bias[0], y = rd[e].hi() + bias[1];
+            if (a.in.softplus) softplus2(x, y);
+            if (row > rmax) x = y = 0.f;  // decay 1, nothing added
+            const float xu = row > rmax ? 0.f : x * cu[e].lo();
+            const float yu = row > rmax ? 0.f : y * cu[e].hi();
+            dtu[row][2 * pr] = make_ulonglong2(pack(x, x), pack(xu, xu));
+            dtu[row][2 * pr + 1] = make_ulonglong2(pack(y, y), pack(yu, yu));
         }
 #pragma unroll
         for (int e = 0; e < EB; ++e) {
-            const int idx = e * NT + tid;
-            if (idx < TT * NP) {
-                (&bc[0][0][0])[idx] = to_f32(rB[e]);
-                if (MODE == 0) (&bc[1][0][0])[idx] = to_f32(rC[e]);
+            const int row = brow + e * RB;
+            if (TT % RB == 0 || row < TT) {
+                bs[row][bm] = bm_ok && row <= rmax ? to_f32(rB[e]) : 0.f;
+                if (MODE == 0) cs[row][bm] = bm_ok && row <= rmax ? to_f32(rC[e]) : 0.f;
             }
         }
         __syncthreads();
-        if (t + TT < t1) load(t + TT);
-#pragma unroll 1
+        const int here = rmax;
+        if (t + TT < t1) {
+            rmax = (int)(t1 - t - TT < TT ? t1 - t - TT : TT) - 1;
+            load(rmax);
+        }
+#pragma unroll 2
         for (int tb = 0; tb < TT; tb += 8) {
-            float acc[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float2 d = dtu[tb + q][sch];
-                const float4 b4 = *reinterpret_cast<const float4*>(&bc[0][tb + q][m0]);
-                const float bv[S] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                for (int i = 0; i < S; ++i) h[i] = fmaf(ex2(d.x * A2[i]), h[i], d.y * bv[i]);
+                const ulonglong2 d = dtu[tb + q][sch];
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&bs[tb + q][m0]);
+                h01 = fma2(ex2_2(mul2(d.x, A01)), h01, mul2(d.y, b.x));
+                h23 = fma2(ex2_2(mul2(d.x, A23)), h23, mul2(d.y, b.y));
                 if (MODE == 0) {
-                    const float4 c4 = *reinterpret_cast<const float4*>(&bc[1][tb + q][m0]);
-                    acc[q] = fmaf(c4.x, h[0], c4.y * h[1]) + fmaf(c4.z, h[2], c4.w * h[3]);
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&cs[tb + q][m0]);
+                    float lo, hi;
+                    unpack(fma2(c.y, h23, mul2(c.x, h01)), lo, hi);
+                    ys[tb + q][tid] = lo + hi;
                 } else {
-                    dts += d.x;
-                }
-            }
-            if (MODE == 0) {
-                lane_reduce<8, K, 1>(acc, lane);
-                if (reduced_writer<8, K, 1>(lane)) {
-                    const int at = reduced_index<8, K, 1>(lane);
-#pragma unroll
-                    for (int r = 0; r < R; ++r) ys[tb + at + r][sch] = acc[r];
+                    float dt, dt_;
+                    unpack(d.x, dt, dt_);
+                    dts += dt;
                 }
             }
         }
         __syncthreads();
-        if (MODE == 0 && ec_ok) {
+        if (MODE == 0) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int row = e * K + etok;
-                const long long tok = t + row;
-                if (tok < t1) {
-                    float y = fmaf(Dw, cu[e], ys[row][ech]);
-                    if (zp) y *= cz[e] * sigmoid_f(cz[e]);
-                    if (a.out_f32) ((float*)a.y)[tok * a.D + ec] = y;
-                    else ((__nv_bfloat16*)a.y)[tok * a.D + ec] = __float2bfloat16_rn(y);
+                const int row = prow + e * RP;
+                float y[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    y[0] += ys[row][2 * pr * K + k];
+                    y[1] += ys[row][(2 * pr + 1) * K + k];
+                }
+                y[0] = fmaf(Dw[0], cu[e].lo(), y[0]);
+                y[1] = fmaf(Dw[1], cu[e].hi(), y[1]);
+                if (gated) {
+                    y[0] *= cz[e].lo() * sigmoid_f(cz[e].lo());
+                    y[1] *= cz[e].hi() * sigmoid_f(cz[e].hi());
+                }
+                if (row <= here) {
+                    const long long at = (t + row) * a.D + ec;
+                    if (a.out_f32) {
+                        float* o = (float*)a.y + at;
+                        if (vec) {
+                            if (lo_ok) *reinterpret_cast<float2*>(o) = make_float2(y[0], y[1]);
+                        } else {
+                            if (lo_ok) o[0] = y[0];
+                            if (hi_ok) o[1] = y[1];
+                        }
+                    } else {
+                        __nv_bfloat16* o = (__nv_bfloat16*)a.y + at;
+                        if (vec) {
+                            if (lo_ok)
+                                *reinterpret_cast<__nv_bfloat162*>(o) =
+                                    __floats2bfloat162_rn(y[0], y[1]);
+                        } else {
+                            if (lo_ok) o[0] = __float2bfloat16_rn(y[0]);
+                            if (hi_ok) o[1] = __float2bfloat16_rn(y[1]);
+                        }
+                    }
                 }
             }
         }
     }
     if (!sc_ok) return;
+    unpack(h01, h[0], h[1]);
+    unpack(h23, h[2], h[3]);
     if (MODE == 1) {
         store_states(a.local + slot, h, m0, a.n);
         if (m0 == 0) a.dtsum[(long long)item * a.D + sc] = dts;
     } else if (last && a.state_out) {
         store_states(a.state_out + ((long long)s * a.D + sc) * a.n, h, m0, a.n);
     }
+}
+
+template <int K> constexpr int scan_smem(int mode)
+{
+    const int TT = K == 1 ? 8 : K == 2 ? 16 : 32;
+    return TT * (NT / K * 16 + 2 * SCAN_S * K * 4 + (mode == 0 ? NT * 4 : 0));
 }
 
 // One token per sequence: the states are the traffic, one vector of four per
@@ -303,19 +399,23 @@ struct ForwardPlan {
     int items;
 };
 
-// How the forward scan is cut. GPU_WARPS: four schedulers on 148 SMs.
-ForwardPlan plan_forward(int G, int D, long long total, int n, int num_seqs)
+// How the forward scan is cut. One warp on each of the GPU's 592 schedulers is
+// what a scan should have at least; chunks are made for two. A packed batch's
+// lengths are not known here, so that it counts as one long sequence: where its
+// sequences are shorter than a chunk, the first launch finds nothing to do.
+ForwardPlan plan_forward(bool packed, int G, int D, long long total, int n, int num_seqs)
 {
-    constexpr long long GPU_WARPS = 148 * 4;
+    constexpr long long SCHEDULERS = 148 * 4;
     const int K = scan_lanes(n), CC = NT / K;
-    const long long blocks = (long long)G * ((D / G + CC - 1) / CC);
-    const long long warps = blocks * (NT / 32);
-    if (num_seqs == 0 || warps * num_seqs >= GPU_WARPS) return {0, num_seqs};
-    long long want = (2 * GPU_WARPS + warps - 1) / warps;  // chunks
+    const long long warps = (long long)G * ((D / G + CC - 1) / CC) * (NT / 32);
+    if (num_seqs == 0 || total == 0 || (packed ? 1 : num_seqs) * warps >= SCHEDULERS)
+        return {0, num_seqs};
+    long long want = (2 * SCHEDULERS + warps - 1) / warps;  // chunks in all
     if (want > 64) want = 64;
     long long len = ((total + want - 1) / want + 31) / 32 * 32;
     if (len < 64) len = 64;
-    if (len * num_seqs >= total && total / num_seqs * 2 < len * 3) return {0, num_seqs};
+    // Below three chunks the second walk costs what the cut gains.
+    if ((packed ? total : total / num_seqs) <= 2 * len) return {0, num_seqs};
     return {len, (int)(total / len + num_seqs)};
 }
 
@@ -334,7 +434,8 @@ size_t scan_backward_workspace(int G, int D, long long total, int n, int num_seq
 size_t scan_workspace(bool backward, int G, int D, long long total, int n, int num_seqs)
 {
     if (backward) return scan_backward_workspace(G, D, total, n, num_seqs);
-    const ForwardPlan f = plan_forward(G, D, total, n, num_seqs);
+    // The larger of what a packed and a dense batch take.
+    const ForwardPlan f = plan_forward(true, G, D, total, n, num_seqs);
     if (f.len == 0) return 0;
     return align_up((size_t)f.items * D * n * 4, 256) + align_up((size_t)f.items * D * 4, 256) +
            align_up((size_t)(num_seqs + 1 + f.items) * 4, 256);
@@ -355,7 +456,14 @@ cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, fl
     a.n = p.n;
     a.cpg = (Dg + CC - 1) / CC;
     a.out_f32 = p.out_t == LA_F32;
-    const ForwardPlan f = plan_forward(p.G, p.D, p.view.total, p.n, p.view.num_seqs);
+    const size_t two = p.in_t == LA_BF16 ? 4 : 8;  // bytes of a pair of channels
+    const auto pairs = [&](const void* q, long long ld) {
+        return (uintptr_t)q % two == 0 && ld % 2 == 0;
+    };
+    a.vec = Dg % 2 == 0 && pairs(p.in.u, p.in.ld_u) && pairs(p.in.delta, p.in.ld_delta) &&
+            (!p.in.z || pairs(p.in.z, p.in.ld_z));
+    const ForwardPlan f = plan_forward(p.view.cu != nullptr, p.G, p.D, p.view.total, p.n,
+                                       p.view.num_seqs);
     a.ch.len = LLONG_MAX / 2;
     a.ch.items = p.view.num_seqs;
     if (f.len) {
@@ -382,11 +490,12 @@ cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, fl
     const unsigned grid = (unsigned)((long long)a.ch.items * a.G * a.cpg);
 #define LA_CALL(KK)                                                                              \
     if (p.in_t == LA_BF16) {                                                                     \
-        if (f.len) scan_kernel<__nv_bfloat16, KK, 1><<<grid, NT, 0, stream>>>(a);                \
-        scan_kernel<__nv_bfloat16, KK, 0><<<grid, NT, 0, stream>>>(a);                           \
+        if (f.len)                                                                               \
+            scan_kernel<__nv_bfloat16, KK, 1><<<grid, NT, scan_smem<KK>(1), stream>>>(a);        \
+        scan_kernel<__nv_bfloat16, KK, 0><<<grid, NT, scan_smem<KK>(0), stream>>>(a);            \
     } else {                                                                                     \
-        if (f.len) scan_kernel<float, KK, 1><<<grid, NT, 0, stream>>>(a);                        \
-        scan_kernel<float, KK, 0><<<grid, NT, 0, stream>>>(a);                                   \
+        if (f.len) scan_kernel<float, KK, 1><<<grid, NT, scan_smem<KK>(1), stream>>>(a);         \
+        scan_kernel<float, KK, 0><<<grid, NT, scan_smem<KK>(0), stream>>>(a);                    \
     }
     LA_SCAN_DISPATCH_K(p.n, LA_CALL)
 #undef LA_CALL

@@ -23,25 +23,108 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Pairs of fp32 in one 64-bit register, for the packed instructions: one issue
+// slot for two operations.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float a, float b)
+{
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f2 v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b)
+{
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 x)
+{
+    float a, b;
+    unpack(x, a, b);
+    return pack(ex2(a), ex2(b));
+}
+
+// sigmoid(x) = 1 / (1 + 2^(-x log2 e)); a large negative x gives 1 / inf = 0.
+__device__ __forceinline__ float sigmoid_f(float x)
+{
+    return rcp(1.f + ex2(-SCAN_LOG2E * x));
+}
+
+// exp(-|x|): the product |x| log2 e is rounded to fp32, an error of up to
+// 2^-24 |x| log2 e in the exponent; its rest, from one multiply-add more, is put
+// back by a first-order factor. Beyond 100 the result counts as e^-100, which
+// spares the case of an infinite product (and a NaN stays one).
+__device__ __forceinline__ float exp_neg_abs(float x)
+{
+    constexpr float LO = 1.9259629e-8f;  // log2 e - fp32(log2 e)
+    float t = fabsf(x);
+    t = t > 100.f ? 100.f : t;
+    const float hi = -SCAN_LOG2E * t;
+    const float lo = fmaf(-LO, t, fmaf(-SCAN_LOG2E, t, -hi));
+    const float e = ex2(hi);
+    return fmaf(e, lo * SCAN_LN2, e);
+}
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) <= 1. The logarithm by
 // log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and the series of atanh: its
 // terms are positive, so small results keep their relative precision (the
-// first term left out is below 2^-25 of the sum).
+// first term left out is below 2^-25 of the sum). Its derivative, sigmoid(x),
+// is 1 / (1 + e) or e / (1 + e).
+__device__ __forceinline__ f2 atanh_series(f2 q)
+{
+    f2 p = pack(1.f / 15, 1.f / 15);
+    p = fma2(p, q, pack(1.f / 13, 1.f / 13));
+    p = fma2(p, q, pack(1.f / 11, 1.f / 11));
+    p = fma2(p, q, pack(1.f / 9, 1.f / 9));
+    p = fma2(p, q, pack(1.f / 7, 1.f / 7));
+    p = fma2(p, q, pack(1.f / 5, 1.f / 5));
+    p = fma2(p, q, pack(1.f / 3, 1.f / 3));
+    return fma2(p, q, pack(1.f, 1.f));
+}
+__device__ __forceinline__ void softplus2(float& x, float& y)
+{
+    const float ex = exp_neg_abs(x), ey = exp_neg_abs(y);
+    const f2 s = mul2(pack(ex, ey), pack(rcp(2.f + ex), rcp(2.f + ey)));
+    float px, py;
+    unpack(mul2(s, atanh_series(mul2(s, s))), px, py);
+    x = fmaf(2.f, px, fmaxf(x, 0.f));
+    y = fmaf(2.f, py, fmaxf(y, 0.f));
+}
 __device__ __forceinline__ float softplus_f(float x)
 {
-    const float e = __expf(-fabsf(x));
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = 1.f / 15;
-    p = fmaf(p, q, 1.f / 13);
-    p = fmaf(p, q, 1.f / 11);
-    p = fmaf(p, q, 1.f / 9);
-    p = fmaf(p, q, 1.f / 7);
-    p = fmaf(p, q, 1.f / 5);
-    p = fmaf(p, q, 1.f / 3);
-    p = fmaf(p, q, 1.f);
-    return fmaxf(x, 0.f) + 2.f * s * p;
+    float y = 0.f;
+    softplus2(x, y);
+    return x;
+}
+// softplus and its derivative.
+__device__ __forceinline__ float softplus_slope(float x)
+{
+    const float e = exp_neg_abs(x), r = rcp(1.f + e);
+    return x >= 0.f ? r : e * r;
 }
 
 // Sum V values over the M lanes that differ in the bits [STEP, STEP M) of the
