@@ -22,7 +22,7 @@
 namespace la {
 namespace {
 
-constexpr int NT = 128;  // threads per CTA
+constexpr int NT = 128;  // scanning threads per CTA; as many serve them
 
 struct ScanArgs {
     la_scan_inputs in;
@@ -67,75 +67,69 @@ template <> struct Pair<float> {
     __device__ __forceinline__ float hi() const { return y; }
 };
 
+// Named barriers of a CTA: `arrive` counts this warp in without waiting.
+__device__ __forceinline__ void bar_sync(int id)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(2 * NT) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(2 * NT) : "memory");
+}
+
+// A CTA's chunk and channels, the same for all its threads.
+struct Place {
+    int s, chunk, nchunks, item, g, c0, c_end;
+    long long t0, t1;
+};
+
 // MODE 0: with outputs. MODE 1: the chunks' states only.
 //
-// Per tile of TT tokens: each thread turns E pairs of channels into (dt, dt u),
-// each twice in a row as the packed multiplies want them; then every thread
-// scans its four states of one channel over the tile and leaves its share of
-// C . h in shared memory; then the pairs' threads add the K shares, the skip
-// and the gate and store. The next tile's inputs are loaded into registers
-// before the scan, which hides them.
-template <typename T, int K, int MODE>
-__global__ void __launch_bounds__(NT, 4) scan_kernel(ScanArgs a)
+// The CTA's first NT threads scan, the other NT serve them, tile by tile of TT
+// tokens through two sets of shared buffers. The servers turn pairs of channels
+// into (dt, dt u), each twice in a row as the packed multiplies want them; the
+// scanning threads carry four states of one channel each over the tile and
+// leave their shares of C . h; the servers add the K shares, the skip and the
+// gate and store. So the exponentials of the scan run while the next tile is
+// made and the last one stored, and the next inputs are on their way.
+template <int K> struct ScanTile {
+    static constexpr int NP = SCAN_S * K, CC = NT / K;
+    static constexpr int TT = K == 1 ? 8 : K == 2 ? 16 : 32;  // tokens
+    ulonglong2 dtu[TT][CC];
+    float b[TT][NP];
+    float c[TT][NP];
+    float y[TT][NT];
+};
+
+template <int K, int MODE>
+__device__ __forceinline__ void scan_threads(const ScanArgs& a, const Place& p, ScanTile<K>* tiles)
 {
-    constexpr int S = SCAN_S, NP = S * K, CC = NT / K;
-    constexpr int TT = K == 1 ? 8 : K == 2 ? 16 : 32;  // tokens per tile
-    constexpr int RP = 2 * K;                          // rows between a thread's pairs
-    constexpr int E = TT / RP;                         // pairs per thread
-    constexpr int RB = NT / NP, EB = (TT + RB - 1) / RB;
-    constexpr uint32_t TS = sizeof(T);
-    extern __shared__ __align__(16) unsigned char smem[];
-    ulonglong2(*dtu)[CC] = reinterpret_cast<ulonglong2(*)[CC]>(smem);  // [TT][CC]
-    float(*bs)[NP] = reinterpret_cast<float(*)[NP]>(dtu + TT);         // [TT][NP]
-    float(*cs)[NP] = bs + TT;
-    float(*ys)[NT] = reinterpret_cast<float(*)[NT]>(cs + TT);          // [TT][NT]
-
+    constexpr int S = SCAN_S, TT = ScanTile<K>::TT;
     const int tid = threadIdx.x;
-    const int blocks = a.G * a.cpg;
-    const int item = blockIdx.x / blocks, cb = blockIdx.x % blocks;
-    const int s = a.ch.seq(item);
-    if (s < 0) return;
-    const int chunk = item - a.ch.first_of(s), nchunks = a.ch.end_of(s) - a.ch.first_of(s);
-    const bool last = chunk == nchunks - 1;
-    long long t0, t1;
-    a.view.range(s, t0, t1);
-    t0 += chunk * a.ch.len;
-    if (t1 - t0 > a.ch.len) t1 = t0 + a.ch.len;
+    const int sch = tid / K, m0 = (tid % K) * S, sc = p.c0 + sch;
+    const bool ok = sc < p.c_end, last = p.chunk == p.nchunks - 1;
 
-    const int g = cb / a.cpg, Dg = a.D / a.G;
-    const int c0 = g * Dg + (cb % a.cpg) * CC, c_end = (g + 1) * Dg;
-    // scan mapping
-    const int sch = tid / K, m0 = (tid % K) * S, sc = c0 + sch;
-    const bool sc_ok = sc < c_end;
-    // pair mapping; channels behind the group's last read the last ones
-    const int pr = tid % (CC / 2), prow = tid / (CC / 2);
-    const int ec = c0 + 2 * pr;
-    const bool lo_ok = ec < c_end, hi_ok = ec + 1 < c_end;
-    const int ch = lo_ok ? 2 * pr : c_end - c0 - (a.vec ? 2 : 1);
-    const uint32_t ch_at = (uint32_t)ch * TS, next = hi_ok ? TS : 0;
-
-    float A2[S] = {0.f, 0.f, 0.f, 0.f}, h[S] = {0.f, 0.f, 0.f, 0.f};
-    if (sc_ok) load_states(A2, a.in.A + (long long)sc * a.n, m0, a.n);
+    float A[S] = {0.f, 0.f, 0.f, 0.f}, h[S] = {0.f, 0.f, 0.f, 0.f};
+    if (ok) load_states(A, a.in.A + (long long)sc * a.n, m0, a.n);
     const f2 log2e = pack(SCAN_LOG2E, SCAN_LOG2E);
-    const f2 A01 = mul2(pack(A2[0], A2[1]), log2e), A23 = mul2(pack(A2[2], A2[3]), log2e);
-    const long long slot = ((long long)item * a.D + sc) * a.n;
-    if (sc_ok) {
+    const f2 A01 = mul2(pack(A[0], A[1]), log2e), A23 = mul2(pack(A[2], A[3]), log2e);
+    const long long slot = ((long long)p.item * a.D + sc) * a.n;
+    if (ok) {
+        const float* in = a.state_in ? a.state_in + ((long long)p.s * a.D + sc) * a.n : nullptr;
         if (MODE == 1) {
             // The last chunk's slot is free: it keeps the incoming state, which
             // may be overwritten in place before the first chunk reads it.
-            if (a.state_in && (chunk == 0 || last))
-                load_states(h, a.state_in + ((long long)s * a.D + sc) * a.n, m0, a.n);
+            if (in && (p.chunk == 0 || last)) load_states(h, in, m0, a.n);
             if (last) store_states(a.local + slot, h, m0, a.n);
-        } else if (nchunks == 1) {
-            if (a.state_in)
-                load_states(h, a.state_in + ((long long)s * a.D + sc) * a.n, m0, a.n);
-        } else if (chunk == 0) {
-            load_states(h, a.local + slot + (long long)(nchunks - 1) * a.D * a.n, m0, a.n);
+        } else if (p.nchunks == 1) {
+            if (in) load_states(h, in, m0, a.n);
+        } else if (p.chunk == 0) {
+            load_states(h, a.local + slot + (long long)(p.nchunks - 1) * a.D * a.n, m0, a.n);
         } else {
-            const long long first = (long long)a.ch.first_of(s) * a.D + sc;
+            const long long first = (long long)(p.item - p.chunk) * a.D + sc;
             load_states(h, a.local + first * a.n, m0, a.n);
 #pragma unroll 4
-            for (int c = 1; c < chunk; ++c) {
+            for (int c = 1; c < p.chunk; ++c) {
                 float l[S], e[S];
                 load_states(l, a.local + (first + (long long)c * a.D) * a.n, m0, a.n);
                 const float d = a.dtsum[first + (long long)c * a.D];
@@ -147,16 +141,68 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(ScanArgs a)
         }
     }
     if (MODE == 1 && last) return;
-    f2 h01 = pack(h[0], h[1]), h23 = pack(h[2], h[3]);
+    f2 h01 = pack(h[0], h[1]), h23 = pack(h[2], h[3]), dts = pack(0.f, 0.f);
+    int turn = 0;
+#pragma unroll 1
+    for (long long t = p.t0; t < p.t1; t += TT, turn ^= 1) {
+        ScanTile<K>& w = tiles[turn];
+        bar_sync(1 + turn);
+#pragma unroll 2
+        for (int tb = 0; tb < TT; tb += 8) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const ulonglong2 d = w.dtu[tb + q][sch];
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&w.b[tb + q][m0]);
+                h01 = fma2(ex2_2(mul2(d.x, A01)), h01, mul2(d.y, b.x));
+                h23 = fma2(ex2_2(mul2(d.x, A23)), h23, mul2(d.y, b.y));
+                if (MODE == 0) {
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&w.c[tb + q][m0]);
+                    float lo, hi;
+                    unpack(fma2(c.y, h23, mul2(c.x, h01)), lo, hi);
+                    w.y[tb + q][tid] = lo + hi;
+                } else {
+                    dts = add2(dts, d.x);
+                }
+            }
+        }
+        bar_arrive(3 + turn);
+    }
+    if (!ok) return;
+    unpack(h01, h[0], h[1]);
+    unpack(h23, h[2], h[3]);
+    if (MODE == 1) {
+        float d, d_;
+        unpack(dts, d, d_);
+        store_states(a.local + slot, h, m0, a.n);
+        if (m0 == 0) a.dtsum[(long long)p.item * a.D + sc] = d;
+    } else if (last && a.state_out) {
+        store_states(a.state_out + ((long long)p.s * a.D + sc) * a.n, h, m0, a.n);
+    }
+}
 
+template <typename T, int K, int MODE>
+__device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p, ScanTile<K>* tiles)
+{
+    constexpr int NP = ScanTile<K>::NP, CC = ScanTile<K>::CC, TT = ScanTile<K>::TT;
+    constexpr int RP = 2 * K;                       // rows between a thread's pairs
+    constexpr int E = TT / RP;                      // pairs per thread
+    constexpr int RB = NT / NP, EB = (TT + RB - 1) / RB;
+    constexpr uint32_t TS = sizeof(T);
+    const int tid = threadIdx.x - NT;
+    const int pr = tid % (CC / 2), prow = tid / (CC / 2);
+    const int ec = p.c0 + 2 * pr;
+    // Channels behind the group's last read the last ones.
+    const bool lo_ok = ec < p.c_end, hi_ok = ec + 1 < p.c_end;
+    const int ch = lo_ok ? 2 * pr : p.c_end - p.c0 - (a.vec ? 2 : 1);
+    const uint32_t ch_at = (uint32_t)ch * TS, next = hi_ok ? TS : 0;
     const uint32_t lu = (uint32_t)a.in.ld_u * TS, ld = (uint32_t)a.in.ld_delta * TS;
     const uint32_t lz = (uint32_t)a.in.ld_z * TS;
     const uint32_t lb = (uint32_t)a.in.ld_b * TS, lc = (uint32_t)a.in.ld_c * TS;
-    const char* up = (const char*)a.in.u + ((long long)c0 + t0 * a.in.ld_u) * TS;
-    const char* dp = (const char*)a.in.delta + ((long long)c0 + t0 * a.in.ld_delta) * TS;
-    const char* zp = (const char*)a.in.z + ((long long)c0 + t0 * a.in.ld_z) * TS;
-    const char* Bp = (const char*)a.in.B + ((long long)g * a.n + t0 * a.in.ld_b) * TS;
-    const char* Cp = (const char*)a.in.C + ((long long)g * a.n + t0 * a.in.ld_c) * TS;
+    const char* up = (const char*)a.in.u + ((long long)p.c0 + p.t0 * a.in.ld_u) * TS;
+    const char* dp = (const char*)a.in.delta + ((long long)p.c0 + p.t0 * a.in.ld_delta) * TS;
+    const char* zp = (const char*)a.in.z + ((long long)p.c0 + p.t0 * a.in.ld_z) * TS;
+    const char* Bp = (const char*)a.in.B + ((long long)p.g * a.n + p.t0 * a.in.ld_b) * TS;
+    const char* Cp = (const char*)a.in.C + ((long long)p.g * a.n + p.t0 * a.in.ld_c) * TS;
     const bool gated = a.in.z != nullptr, vec = a.vec;
     const int bm = tid % NP, brow = tid / NP;
     const bool bm_ok = bm < a.n;
@@ -171,8 +217,10 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(ScanArgs a)
         if (hi_ok) Dw[1] = a.in.D[ec + 1];
     }
 
-    Pair<T> ru[E], rd[E], rz[E];
+    // Loaded for the next tile; of this tile and of the last one.
+    Pair<T> ru[E], rd[E], rz[E], cu[E], cz[E], pu[E], pz[E];
     T rB[EB], rC[EB];
+    // Rows of a tile are counted from its first; rmax is the last that exists.
     auto load = [&](int rmax) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -193,117 +241,114 @@ __global__ void __launch_bounds__(NT, 4) scan_kernel(ScanArgs a)
         Bp += (long long)TT * lb;
         Cp += (long long)TT * lc;
     };
-
-    float dts = 0.f;
-    // Rows of a tile are counted from its first; rmax is the last that exists.
-    int rmax = (int)(t1 - t0 < TT ? t1 - t0 : TT) - 1;
-    if (t0 < t1) load(rmax);
-    for (long long t = t0; t < t1; t += TT) {
-        Pair<T> cu[E], cz[E];
+    // The outputs of the tile at t, whose shares are in w.
+    auto finish = [&](long long t, const ScanTile<K>& w) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
+            const int row = prow + e * RP;
+            float y[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                y[0] += w.y[row][2 * pr * K + k];
+                y[1] += w.y[row][(2 * pr + 1) * K + k];
+            }
+            y[0] = fmaf(Dw[0], pu[e].lo(), y[0]);
+            y[1] = fmaf(Dw[1], pu[e].hi(), y[1]);
+            if (gated) {
+                y[0] *= pz[e].lo() * sigmoid_f(pz[e].lo());
+                y[1] *= pz[e].hi() * sigmoid_f(pz[e].hi());
+            }
+            if (t + row >= p.t1) continue;
+            const long long at = (t + row) * a.D + ec;
+            if (a.out_f32) {
+                float* o = (float*)a.y + at;
+                if (vec) {
+                    if (lo_ok) *reinterpret_cast<float2*>(o) = make_float2(y[0], y[1]);
+                } else {
+                    if (lo_ok) o[0] = y[0];
+                    if (hi_ok) o[1] = y[1];
+                }
+            } else {
+                __nv_bfloat16* o = (__nv_bfloat16*)a.y + at;
+                if (vec) {
+                    if (lo_ok)
+                        *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(y[0], y[1]);
+                } else {
+                    if (lo_ok) o[0] = __float2bfloat16_rn(y[0]);
+                    if (hi_ok) o[1] = __float2bfloat16_rn(y[1]);
+                }
+            }
+        }
+    };
+
+    int rmax = (int)(p.t1 - p.t0 < TT ? p.t1 - p.t0 : TT) - 1, turn = 0;
+    if (p.t0 < p.t1) load(rmax);
+#pragma unroll 1
+    for (long long t = p.t0; t < p.t1; t += TT, turn ^= 1) {
+        ScanTile<K>& w = tiles[turn];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (MODE == 0) pu[e] = cu[e], pz[e] = cz[e], cz[e] = rz[e];
             cu[e] = ru[e];
-            if (MODE == 0) cz[e] = rz[e];
             const int row = prow + e * RP;
             float x = rd[e].lo() + bias[0], y = rd[e].hi() + bias[1];
             if (a.in.softplus) softplus2(x, y);
-            if (row > rmax) x = y = 0.f;  // decay 1, nothing added
-            const float xu = row > rmax ? 0.f : x * cu[e].lo();
-            const float yu = row > rmax ? 0.f : y * cu[e].hi();
-            dtu[row][2 * pr] = make_ulonglong2(pack(x, x), pack(xu, xu));
-            dtu[row][2 * pr + 1] = make_ulonglong2(pack(y, y), pack(yu, yu));
+            float xu = x * cu[e].lo(), yu = y * cu[e].hi();
+            if (row > rmax) x = y = xu = yu = 0.f;  // decay 1, nothing added
+            w.dtu[row][2 * pr] = make_ulonglong2(pack(x, x), pack(xu, xu));
+            w.dtu[row][2 * pr + 1] = make_ulonglong2(pack(y, y), pack(yu, yu));
         }
 #pragma unroll
         for (int e = 0; e < EB; ++e) {
             const int row = brow + e * RB;
             if (TT % RB == 0 || row < TT) {
-                bs[row][bm] = bm_ok && row <= rmax ? to_f32(rB[e]) : 0.f;
-                if (MODE == 0) cs[row][bm] = bm_ok && row <= rmax ? to_f32(rC[e]) : 0.f;
+                w.b[row][bm] = bm_ok && row <= rmax ? to_f32(rB[e]) : 0.f;
+                if (MODE == 0) w.c[row][bm] = bm_ok && row <= rmax ? to_f32(rC[e]) : 0.f;
             }
         }
-        __syncthreads();
-        const int here = rmax;
-        if (t + TT < t1) {
-            rmax = (int)(t1 - t - TT < TT ? t1 - t - TT : TT) - 1;
+        bar_arrive(1 + turn);
+        if (t + TT < p.t1) {
+            rmax = (int)(p.t1 - t - TT < TT ? p.t1 - t - TT : TT) - 1;
             load(rmax);
         }
-#pragma unroll 2
-        for (int tb = 0; tb < TT; tb += 8) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const ulonglong2 d = dtu[tb + q][sch];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&bs[tb + q][m0]);
-                h01 = fma2(ex2_2(mul2(d.x, A01)), h01, mul2(d.y, b.x));
-                h23 = fma2(ex2_2(mul2(d.x, A23)), h23, mul2(d.y, b.y));
-                if (MODE == 0) {
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&cs[tb + q][m0]);
-                    float lo, hi;
-                    unpack(fma2(c.y, h23, mul2(c.x, h01)), lo, hi);
-                    ys[tb + q][tid] = lo + hi;
-                } else {
-                    float dt, dt_;
-                    unpack(d.x, dt, dt_);
-                    dts += dt;
-                }
-            }
-        }
-        __syncthreads();
-        if (MODE == 0) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int row = prow + e * RP;
-                float y[2] = {0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    y[0] += ys[row][2 * pr * K + k];
-                    y[1] += ys[row][(2 * pr + 1) * K + k];
-                }
-                y[0] = fmaf(Dw[0], cu[e].lo(), y[0]);
-                y[1] = fmaf(Dw[1], cu[e].hi(), y[1]);
-                if (gated) {
-                    y[0] *= cz[e].lo() * sigmoid_f(cz[e].lo());
-                    y[1] *= cz[e].hi() * sigmoid_f(cz[e].hi());
-                }
-                if (row <= here) {
-                    const long long at = (t + row) * a.D + ec;
-                    if (a.out_f32) {
-                        float* o = (float*)a.y + at;
-                        if (vec) {
-                            if (lo_ok) *reinterpret_cast<float2*>(o) = make_float2(y[0], y[1]);
-                        } else {
-                            if (lo_ok) o[0] = y[0];
-                            if (hi_ok) o[1] = y[1];
-                        }
-                    } else {
-                        __nv_bfloat16* o = (__nv_bfloat16*)a.y + at;
-                        if (vec) {
-                            if (lo_ok)
-                                *reinterpret_cast<__nv_bfloat162*>(o) =
-                                    __floats2bfloat162_rn(y[0], y[1]);
-                        } else {
-                            if (lo_ok) o[0] = __float2bfloat16_rn(y[0]);
-                            if (hi_ok) o[1] = __float2bfloat16_rn(y[1]);
-                        }
-                    }
-                }
-            }
+        // The scan is done with the other set: it may be stored and filled again.
+        if (t > p.t0) {
+            bar_sync(3 + (turn ^ 1));
+            if (MODE == 0) finish(t - TT, tiles[turn ^ 1]);
         }
     }
-    if (!sc_ok) return;
-    unpack(h01, h[0], h[1]);
-    unpack(h23, h[2], h[3]);
-    if (MODE == 1) {
-        store_states(a.local + slot, h, m0, a.n);
-        if (m0 == 0) a.dtsum[(long long)item * a.D + sc] = dts;
-    } else if (last && a.state_out) {
-        store_states(a.state_out + ((long long)s * a.D + sc) * a.n, h, m0, a.n);
+    if (p.t0 < p.t1) {
+        const int final_turn = turn ^ 1;
+        bar_sync(3 + final_turn);
+        if (MODE == 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) pu[e] = cu[e], pz[e] = cz[e];
+            finish(p.t0 + (p.t1 - p.t0 - 1) / TT * TT, tiles[final_turn]);
+        }
     }
 }
 
-template <int K> constexpr int scan_smem(int mode)
+template <typename T, int K, int MODE>
+__global__ void __launch_bounds__(2 * NT, 2) scan_kernel(ScanArgs a)
 {
-    const int TT = K == 1 ? 8 : K == 2 ? 16 : 32;
-    return TT * (NT / K * 16 + 2 * SCAN_S * K * 4 + (mode == 0 ? NT * 4 : 0));
+    extern __shared__ __align__(16) unsigned char smem[];
+    ScanTile<K>* tiles = reinterpret_cast<ScanTile<K>*>(smem);
+    const int blocks = a.G * a.cpg, cb = blockIdx.x % blocks, Dg = a.D / a.G;
+    Place p;
+    p.item = blockIdx.x / blocks;
+    p.s = a.ch.seq(p.item);
+    if (p.s < 0) return;
+    const int first = a.ch.first_of(p.s);
+    p.chunk = p.item - first;
+    p.nchunks = a.ch.end_of(p.s) - first;
+    a.view.range(p.s, p.t0, p.t1);
+    p.t0 += p.chunk * a.ch.len;
+    if (p.t1 - p.t0 > a.ch.len) p.t1 = p.t0 + a.ch.len;
+    p.g = cb / a.cpg;
+    p.c0 = p.g * Dg + (cb % a.cpg) * ScanTile<K>::CC;
+    p.c_end = (p.g + 1) * Dg;
+    if (threadIdx.x < NT) scan_threads<K, MODE>(a, p, tiles);
+    else if (MODE == 0 || p.chunk < p.nchunks - 1) serve_threads<T, K, MODE>(a, p, tiles);
 }
 
 // One token per sequence: the states are the traffic, one vector of four per
@@ -419,6 +464,23 @@ ForwardPlan plan_forward(bool packed, int G, int D, long long total, int n, int 
     return {len, (int)(total / len + num_seqs)};
 }
 
+// The pass over the chunks' states (if any) and the pass with outputs.
+template <int K>
+cudaError_t launch_tiles(void (*states)(ScanArgs), void (*outputs)(ScanArgs), const ScanArgs& a,
+                         unsigned grid, cudaStream_t stream)
+{
+    constexpr int smem = 2 * (int)sizeof(ScanTile<K>);
+    for (auto kernel : {states, outputs}) {
+        if (!kernel) continue;
+        cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, 2 * NT, smem, stream>>>(a);
+        count_launch();
+    }
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_plan_chunks(const SeqView& v, long long len, int items, int* first, int* seq_of,
@@ -488,19 +550,19 @@ cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, fl
         }
     }
     const unsigned grid = (unsigned)((long long)a.ch.items * a.G * a.cpg);
+    cudaError_t e = cudaSuccess;
 #define LA_CALL(KK)                                                                              \
-    if (p.in_t == LA_BF16) {                                                                     \
-        if (f.len)                                                                               \
-            scan_kernel<__nv_bfloat16, KK, 1><<<grid, NT, scan_smem<KK>(1), stream>>>(a);        \
-        scan_kernel<__nv_bfloat16, KK, 0><<<grid, NT, scan_smem<KK>(0), stream>>>(a);            \
-    } else {                                                                                     \
-        if (f.len) scan_kernel<float, KK, 1><<<grid, NT, scan_smem<KK>(1), stream>>>(a);         \
-        scan_kernel<float, KK, 0><<<grid, NT, scan_smem<KK>(0), stream>>>(a);                    \
-    }
+    do {                                                                                         \
+        const bool low = p.in_t == LA_BF16;                                                      \
+        e = launch_tiles<KK>(f.len ? (low ? scan_kernel<__nv_bfloat16, KK, 1>                    \
+                                          : scan_kernel<float, KK, 1>)                           \
+                                   : nullptr,                                                    \
+                             low ? scan_kernel<__nv_bfloat16, KK, 0> : scan_kernel<float, KK, 0>, \
+                             a, grid, stream);                                                   \
+    } while (0)
     LA_SCAN_DISPATCH_K(p.n, LA_CALL)
 #undef LA_CALL
-    count_launch(f.len ? 2 : 1);
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_scan_step(const ScanProblem& p, float* state, void* y, cudaStream_t stream)
