@@ -123,13 +123,6 @@ __device__ __forceinline__ void load_weights(const float* weight, const float* b
     }
 }
 
-__device__ __forceinline__ f2 sigmoid2(f2 x)
-{
-    float a, b;
-    unpack(add2(ex2_2(mul2(x, pack(-SCAN_LOG2E, -SCAN_LOG2E))), pack(1.f, 1.f)), a, b);
-    return pack(rcp(a), rcp(b));
-}
-
 // CTAs [0, tiles * cblocks) convolve; the CTAs behind them write state_out.
 template <typename T, typename To, int W, int V>
 __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a)

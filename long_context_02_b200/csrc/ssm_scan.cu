@@ -22,7 +22,7 @@
 namespace la {
 namespace {
 
-constexpr int NT = 128;  // scanning threads per CTA; as many serve them
+constexpr int NT = 128;  // scanning threads per CTA
 
 struct ScanArgs {
     la_scan_inputs in;
@@ -34,47 +34,43 @@ struct ScanArgs {
     float* local;   // [items][D][n], chunked only
     float* dtsum;   // [items][D]
     int D, G, n, cpg;  // cpg: channel blocks per group
-    int out_f32, vec;
+    int out_f32;
 };
 
-// Two adjacent channels of a token as loaded: one access where `vec` (every
-// row of every tensor then starts on such a pair), else two.
-template <typename T> struct Pair;
-template <> struct Pair<__nv_bfloat16> {
+// Two adjacent channels of a token as loaded: one access where VEC (every row
+// of every tensor then starts on such a pair), else two.
+template <typename T, bool VEC> struct Pair;
+template <bool VEC> struct Pair<__nv_bfloat16, VEC> {
     uint32_t w;
-    __device__ __forceinline__ void load(const char* base, uint32_t at, uint32_t next, bool vec)
+    __device__ __forceinline__ void load(const char* p, uint32_t next)
     {
-        if (vec) w = *reinterpret_cast<const uint32_t*>(base + at);
-        else w = *reinterpret_cast<const uint16_t*>(base + at) |
-                 (uint32_t) * reinterpret_cast<const uint16_t*>(base + at + next) << 16;
+        if (VEC) w = *reinterpret_cast<const uint32_t*>(p);
+        else w = *reinterpret_cast<const uint16_t*>(p) |
+                 (uint32_t) * reinterpret_cast<const uint16_t*>(p + next) << 16;
     }
-    __device__ __forceinline__ float lo() const { return __uint_as_float(w << 16); }
-    __device__ __forceinline__ float hi() const { return __uint_as_float(w & 0xffff0000u); }
+    __device__ __forceinline__ f2 get() const
+    {
+        return pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
 };
-template <> struct Pair<float> {
-    float x, y;
-    __device__ __forceinline__ void load(const char* base, uint32_t at, uint32_t next, bool vec)
+template <bool VEC> struct Pair<float, VEC> {
+    f2 v;
+    __device__ __forceinline__ void load(const char* p, uint32_t next)
     {
-        if (vec) {
-            const float2 v = *reinterpret_cast<const float2*>(base + at);
-            x = v.x, y = v.y;
-        } else {
-            x = *reinterpret_cast<const float*>(base + at);
-            y = *reinterpret_cast<const float*>(base + at + next);
-        }
+        if (VEC) v = *reinterpret_cast<const f2*>(p);
+        else v = pack(*reinterpret_cast<const float*>(p), *reinterpret_cast<const float*>(p + next));
     }
-    __device__ __forceinline__ float lo() const { return x; }
-    __device__ __forceinline__ float hi() const { return y; }
+    __device__ __forceinline__ f2 get() const { return v; }
 };
 
 // Named barriers of a CTA: `arrive` counts this warp in without waiting.
-__device__ __forceinline__ void bar_sync(int id)
+template <int THREADS> __device__ __forceinline__ void bar_sync(int id)
 {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(2 * NT) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(int id)
+template <int THREADS> __device__ __forceinline__ void bar_arrive(int id)
 {
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(2 * NT) : "memory");
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
 
 // A CTA's chunk and channels, the same for all its threads.
@@ -83,118 +79,156 @@ struct Place {
     long long t0, t1;
 };
 
-// MODE 0: with outputs. MODE 1: the chunks' states only.
-//
-// The CTA's first NT threads scan, the other NT serve them, tile by tile of TT
-// tokens through two sets of shared buffers. The servers turn pairs of channels
-// into (dt, dt u), each twice in a row as the packed multiplies want them; the
-// scanning threads carry four states of one channel each over the tile and
-// leave their shares of C . h; the servers add the K shares, the skip and the
-// gate and store. So the exponentials of the scan run while the next tile is
-// made and the last one stored, and the next inputs are on their way.
+// One of the CTA's two sets of buffers, for TT tokens of CC channels: K lanes
+// share two adjacent channels.
 template <int K> struct ScanTile {
-    static constexpr int NP = SCAN_S * K, CC = NT / K;
-    static constexpr int TT = K == 1 ? 8 : K == 2 ? 16 : 32;  // tokens
-    ulonglong2 dtu[TT][CC];
+    static constexpr int NP = SCAN_S * K, CC = 2 * NT / K;
+    static constexpr int TT = K == 1 ? 8 : K == 2 ? 16 : 32;
+    float4 dt[TT][CC / 2];  // dt, dt u of the pair's first channel, then of its second
     float b[TT][NP];
     float c[TT][NP];
-    float y[TT][NT];
+    f2 y[TT][NT];           // each scanning thread's share of C . h, for both channels
 };
 
-template <int K, int MODE>
+template <int K, int MODE, int SV>
 __device__ __forceinline__ void scan_threads(const ScanArgs& a, const Place& p, ScanTile<K>* tiles)
 {
     constexpr int S = SCAN_S, TT = ScanTile<K>::TT;
     const int tid = threadIdx.x;
-    const int sch = tid / K, m0 = (tid % K) * S, sc = p.c0 + sch;
-    const bool ok = sc < p.c_end, last = p.chunk == p.nchunks - 1;
+    const int pr = tid / K, m0 = (tid % K) * S, c0 = p.c0 + 2 * pr;
+    const bool last = p.chunk == p.nchunks - 1;
 
-    float A[S] = {0.f, 0.f, 0.f, 0.f}, h[S] = {0.f, 0.f, 0.f, 0.f};
-    if (ok) load_states(A, a.in.A + (long long)sc * a.n, m0, a.n);
-    const f2 log2e = pack(SCAN_LOG2E, SCAN_LOG2E);
-    const f2 A01 = mul2(pack(A[0], A[1]), log2e), A23 = mul2(pack(A[2], A[3]), log2e);
-    const long long slot = ((long long)p.item * a.D + sc) * a.n;
-    if (ok) {
-        const float* in = a.state_in ? a.state_in + ((long long)p.s * a.D + sc) * a.n : nullptr;
+    float A[2][S], h[2][S];
+    float* const local = a.local;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) A[x][i] = h[x][i] = 0.f;
+        const int c = c0 + x;
+        if (c >= p.c_end) continue;
+        load_states(A[x], a.in.A + (long long)c * a.n, m0, a.n);
+#pragma unroll
+        for (int i = 0; i < S; ++i) A[x][i] *= SCAN_LOG2E;
+        const float* in = a.state_in ? a.state_in + ((long long)p.s * a.D + c) * a.n : nullptr;
+        const long long slot = ((long long)p.item * a.D + c) * a.n;
         if (MODE == 1) {
             // The last chunk's slot is free: it keeps the incoming state, which
             // may be overwritten in place before the first chunk reads it.
-            if (in && (p.chunk == 0 || last)) load_states(h, in, m0, a.n);
-            if (last) store_states(a.local + slot, h, m0, a.n);
+            if (in && (p.chunk == 0 || last)) load_states(h[x], in, m0, a.n);
+            if (last) store_states(local + slot, h[x], m0, a.n);
         } else if (p.nchunks == 1) {
-            if (in) load_states(h, in, m0, a.n);
+            if (in) load_states(h[x], in, m0, a.n);
         } else if (p.chunk == 0) {
-            load_states(h, a.local + slot + (long long)(p.nchunks - 1) * a.D * a.n, m0, a.n);
+            load_states(h[x], local + slot + (long long)(p.nchunks - 1) * a.D * a.n, m0, a.n);
         } else {
-            const long long first = (long long)(p.item - p.chunk) * a.D + sc;
-            load_states(h, a.local + first * a.n, m0, a.n);
+            const long long first = (long long)(p.item - p.chunk) * a.D + c;
+            load_states(h[x], local + first * a.n, m0, a.n);
 #pragma unroll 4
-            for (int c = 1; c < p.chunk; ++c) {
-                float l[S], e[S];
-                load_states(l, a.local + (first + (long long)c * a.D) * a.n, m0, a.n);
-                const float d = a.dtsum[first + (long long)c * a.D];
-                unpack(ex2_2(mul2(pack(d, d), A01)), e[0], e[1]);
-                unpack(ex2_2(mul2(pack(d, d), A23)), e[2], e[3]);
+            for (int k = 1; k < p.chunk; ++k) {
+                float l[S];
+                load_states(l, local + (first + (long long)k * a.D) * a.n, m0, a.n);
+                const float d = a.dtsum[first + (long long)k * a.D];
 #pragma unroll
-                for (int i = 0; i < S; ++i) h[i] = fmaf(e[i], h[i], l[i]);
+                for (int i = 0; i < S; ++i) h[x][i] = fmaf(ex2(d * A[x][i]), h[x][i], l[i]);
             }
         }
     }
     if (MODE == 1 && last) return;
-    f2 h01 = pack(h[0], h[1]), h23 = pack(h[2], h[3]), dts = pack(0.f, 0.f);
+    f2 hp[2][2], Ap[2][2], dts = pack(0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        hp[x][0] = pack(h[x][0], h[x][1]), hp[x][1] = pack(h[x][2], h[x][3]);
+        Ap[x][0] = pack(A[x][0], A[x][1]), Ap[x][1] = pack(A[x][2], A[x][3]);
+    }
     int turn = 0;
 #pragma unroll 1
     for (long long t = p.t0; t < p.t1; t += TT, turn ^= 1) {
         ScanTile<K>& w = tiles[turn];
-        bar_sync(1 + turn);
-#pragma unroll 2
-        for (int tb = 0; tb < TT; tb += 8) {
+        bar_sync<NT + SV>(1 + turn);
+        // The inputs of the next Q tokens are read before the outputs of these
+        // are written: the compiler keeps shared reads behind earlier writes.
+        constexpr int Q = 2;
+        struct In {
+            float4 d;
+            ulonglong2 b, c;
+        } now[Q], then[Q];
+        auto read = [&](int row, In* in) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const ulonglong2 d = w.dtu[tb + q][sch];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&w.b[tb + q][m0]);
-                h01 = fma2(ex2_2(mul2(d.x, A01)), h01, mul2(d.y, b.x));
-                h23 = fma2(ex2_2(mul2(d.x, A23)), h23, mul2(d.y, b.y));
-                if (MODE == 0) {
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&w.c[tb + q][m0]);
-                    float lo, hi;
-                    unpack(fma2(c.y, h23, mul2(c.x, h01)), lo, hi);
-                    w.y[tb + q][tid] = lo + hi;
-                } else {
-                    dts = add2(dts, d.x);
+            for (int q = 0; q < Q; ++q) {
+                in[q].d = w.dt[row + q][pr];
+                in[q].b = *reinterpret_cast<const ulonglong2*>(&w.b[row + q][m0]);
+                if (MODE == 0) in[q].c = *reinterpret_cast<const ulonglong2*>(&w.c[row + q][m0]);
+            }
+        };
+        read(0, then);
+#pragma unroll
+        for (int tb = 0; tb < TT; tb += Q) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) now[q] = then[q];
+            if (tb + Q < TT) read(tb + Q, then);
+            f2 y[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const float4 d = now[q].d;
+                const f2 dt[2] = {pack(d.x, d.x), pack(d.z, d.z)};
+                const f2 du[2] = {pack(d.y, d.y), pack(d.w, d.w)};
+                float yx[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    hp[x][0] = fma2(ex2_2(mul2(dt[x], Ap[x][0])), hp[x][0], mul2(du[x], now[q].b.x));
+                    hp[x][1] = fma2(ex2_2(mul2(dt[x], Ap[x][1])), hp[x][1], mul2(du[x], now[q].b.y));
+                    if (MODE == 0) {
+                        float lo, hi;
+                        unpack(fma2(now[q].c.y, hp[x][1], mul2(now[q].c.x, hp[x][0])), lo, hi);
+                        yx[x] = lo + hi;
+                    }
                 }
+                if (MODE == 0) y[q] = pack(yx[0], yx[1]);
+                else dts = add2(dts, pack(d.x, d.z));
+            }
+            if (MODE == 0) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) w.y[tb + q][tid] = y[q];
             }
         }
-        bar_arrive(3 + turn);
+        bar_arrive<NT + SV>(3 + turn);
     }
-    if (!ok) return;
-    unpack(h01, h[0], h[1]);
-    unpack(h23, h[2], h[3]);
-    if (MODE == 1) {
-        float d, d_;
-        unpack(dts, d, d_);
-        store_states(a.local + slot, h, m0, a.n);
-        if (m0 == 0) a.dtsum[(long long)p.item * a.D + sc] = d;
-    } else if (last && a.state_out) {
-        store_states(a.state_out + ((long long)p.s * a.D + sc) * a.n, h, m0, a.n);
+    float d[2];
+    unpack(dts, d[0], d[1]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int c = c0 + x;
+        if (c >= p.c_end) continue;
+        unpack(hp[x][0], h[x][0], h[x][1]);
+        unpack(hp[x][1], h[x][2], h[x][3]);
+        if (MODE == 1) {
+            store_states(local + ((long long)p.item * a.D + c) * a.n, h[x], m0, a.n);
+            if (m0 == 0) a.dtsum[(long long)p.item * a.D + c] = d[x];
+        } else if (last && a.state_out) {
+            store_states(a.state_out + ((long long)p.s * a.D + c) * a.n, h[x], m0, a.n);
+        }
     }
 }
 
-template <typename T, int K, int MODE>
+template <typename T, int K, int MODE, bool VEC, int SV>
 __device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p, ScanTile<K>* tiles)
 {
-    constexpr int NP = ScanTile<K>::NP, CC = ScanTile<K>::CC, TT = ScanTile<K>::TT;
-    constexpr int RP = 2 * K;                       // rows between a thread's pairs
-    constexpr int E = TT / RP;                      // pairs per thread
-    constexpr int RB = NT / NP, EB = (TT + RB - 1) / RB;
+    using Tile = ScanTile<K>;
+    constexpr int NP = Tile::NP, CP = Tile::CC / 2, TT = Tile::TT;
+    constexpr int RP = SV / CP, E = (TT + RP - 1) / RP;  // rows between a thread's pairs; pairs
+    constexpr int RB = SV / NP, EB = (TT + RB - 1) / RB;
     constexpr uint32_t TS = sizeof(T);
     const int tid = threadIdx.x - NT;
-    const int pr = tid % (CC / 2), prow = tid / (CC / 2);
+    const int pr = tid % CP, prow = tid / CP;
     const int ec = p.c0 + 2 * pr;
     // Channels behind the group's last read the last ones.
     const bool lo_ok = ec < p.c_end, hi_ok = ec + 1 < p.c_end;
-    const int ch = lo_ok ? 2 * pr : p.c_end - p.c0 - (a.vec ? 2 : 1);
-    const uint32_t ch_at = (uint32_t)ch * TS, next = hi_ok ? TS : 0;
+    const int ch = lo_ok ? 2 * pr : p.c_end - p.c0 - (VEC ? 2 : 1);
+    const uint32_t next = hi_ok ? TS : 0;
+    const int bm = tid % NP, brow = tid / NP;
+    const bool bm_ok = bm < a.n;
+    // Addresses are a base that all threads share, which moves from tile to tile
+    // and from row to row, and a thread's own 32-bit offset from it.
     const uint32_t lu = (uint32_t)a.in.ld_u * TS, ld = (uint32_t)a.in.ld_delta * TS;
     const uint32_t lz = (uint32_t)a.in.ld_z * TS;
     const uint32_t lb = (uint32_t)a.in.ld_b * TS, lc = (uint32_t)a.in.ld_c * TS;
@@ -203,37 +237,46 @@ __device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p,
     const char* zp = (const char*)a.in.z + ((long long)p.c0 + p.t0 * a.in.ld_z) * TS;
     const char* Bp = (const char*)a.in.B + ((long long)p.g * a.n + p.t0 * a.in.ld_b) * TS;
     const char* Cp = (const char*)a.in.C + ((long long)p.g * a.n + p.t0 * a.in.ld_c) * TS;
-    const bool gated = a.in.z != nullptr, vec = a.vec;
-    const int bm = tid % NP, brow = tid / NP;
-    const bool bm_ok = bm < a.n;
-    const uint32_t bm_at = (uint32_t)(bm_ok ? bm : 0) * TS;
-    float bias[2] = {0.f, 0.f}, Dw[2] = {0.f, 0.f};
-    if (a.in.delta_bias) {
-        if (lo_ok) bias[0] = a.in.delta_bias[ec];
-        if (hi_ok) bias[1] = a.in.delta_bias[ec + 1];
-    }
-    if (MODE == 0 && a.in.D) {
-        if (lo_ok) Dw[0] = a.in.D[ec];
-        if (hi_ok) Dw[1] = a.in.D[ec + 1];
-    }
+    const uint32_t ch_at = ch * TS, bm_at = (bm_ok ? bm : 0) * TS;
+    const uint32_t ou = prow * lu + ch_at, od = prow * ld + ch_at, oz = prow * lz + ch_at;
+    const uint32_t ob = brow * lb + bm_at, oc = brow * lc + bm_at;
+    const bool gated = MODE == 0 && a.in.z != nullptr;
+    f2 bias = pack(0.f, 0.f), Dw = pack(0.f, 0.f);
+    if (a.in.delta_bias && lo_ok)
+        bias = pack(a.in.delta_bias[ec], hi_ok ? a.in.delta_bias[ec + 1] : 0.f);
+    if (MODE == 0 && a.in.D && lo_ok) Dw = pack(a.in.D[ec], hi_ok ? a.in.D[ec + 1] : 0.f);
 
-    // Loaded for the next tile; of this tile and of the last one.
-    Pair<T> ru[E], rd[E], rz[E], cu[E], cz[E], pu[E], pz[E];
+    Pair<T, VEC> ru[E], rd[E], rz[E], pu[E], pz[E];  // of the next tile; of the last one
     T rB[EB], rC[EB];
-    // Rows of a tile are counted from its first; rmax is the last that exists.
+    // Rows of a tile are counted from its first; rows behind rmax read that one.
     auto load = [&](int rmax) {
+        if (rmax == TT - 1 && TT % RB == 0 && TT % RP == 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t row = min(prow + e * RP, rmax);
-            ru[e].load(up, row * lu + ch_at, next, vec);
-            rd[e].load(dp, row * ld + ch_at, next, vec);
-            if (MODE == 0 && gated) rz[e].load(zp, row * lz + ch_at, next, vec);
-        }
+            for (int e = 0; e < E; ++e) {
+                ru[e].load(up + (long long)(e * RP) * lu + ou, next);
+                rd[e].load(dp + (long long)(e * RP) * ld + od, next);
+                if (gated) rz[e].load(zp + (long long)(e * RP) * lz + oz, next);
+            }
 #pragma unroll
-        for (int e = 0; e < EB; ++e) {
-            const uint32_t row = min(brow + e * RB, rmax);
-            rB[e] = *reinterpret_cast<const T*>(Bp + (row * lb + bm_at));
-            if (MODE == 0) rC[e] = *reinterpret_cast<const T*>(Cp + (row * lc + bm_at));
+            for (int e = 0; e < EB; ++e) {
+                rB[e] = *reinterpret_cast<const T*>(Bp + (long long)(e * RB) * lb + ob);
+                if (MODE == 0)
+                    rC[e] = *reinterpret_cast<const T*>(Cp + (long long)(e * RB) * lc + oc);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint32_t row = min(prow + e * RP, rmax);
+                ru[e].load(up + (row * lu + ch_at), next);
+                rd[e].load(dp + (row * ld + ch_at), next);
+                if (gated) rz[e].load(zp + (row * lz + ch_at), next);
+            }
+#pragma unroll
+            for (int e = 0; e < EB; ++e) {
+                const uint32_t row = min(brow + e * RB, rmax);
+                rB[e] = *reinterpret_cast<const T*>(Bp + (row * lb + bm_at));
+                if (MODE == 0) rC[e] = *reinterpret_cast<const T*>(Cp + (row * lc + bm_at));
+            }
         }
         up += (long long)TT * lu;
         dp += (long long)TT * ld;
@@ -242,40 +285,43 @@ __device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p,
         Cp += (long long)TT * lc;
     };
     // The outputs of the tile at t, whose shares are in w.
-    auto finish = [&](long long t, const ScanTile<K>& w) {
+    auto finish = [&](long long t, const Tile& w) {
+        const int rows = (int)(p.t1 - t < TT ? p.t1 - t : TT);
+        const int os = a.out_f32 ? 4 : 2;
+        char* const out = (char*)a.y + (t * a.D + p.c0) * os;
+        const uint32_t at = (uint32_t)(prow * a.D + 2 * pr) * os;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int row = prow + e * RP;
-            float y[2] = {0.f, 0.f};
+            if (row >= rows || !lo_ok) continue;
+            f2 y;
+            if constexpr (K == 1) {
+                y = w.y[row][pr];
+            } else {
+                const ulonglong2* v = reinterpret_cast<const ulonglong2*>(&w.y[row][pr * K]);
+                y = add2(v[0].x, v[0].y);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                y[0] += w.y[row][2 * pr * K + k];
-                y[1] += w.y[row][(2 * pr + 1) * K + k];
+                for (int k = 1; k < K / 2; ++k) y = add2(y, add2(v[k].x, v[k].y));
             }
-            y[0] = fmaf(Dw[0], pu[e].lo(), y[0]);
-            y[1] = fmaf(Dw[1], pu[e].hi(), y[1]);
+            y = fma2(Dw, pu[e].get(), y);
             if (gated) {
-                y[0] *= pz[e].lo() * sigmoid_f(pz[e].lo());
-                y[1] *= pz[e].hi() * sigmoid_f(pz[e].hi());
+                const f2 z = pz[e].get();
+                y = mul2(y, mul2(z, sigmoid2(z)));
             }
-            if (t + row >= p.t1) continue;
-            const long long at = (t + row) * a.D + ec;
+            char* const o = out + (long long)(e * RP) * a.D * os + at;
+            float lo, hi;
+            unpack(y, lo, hi);
             if (a.out_f32) {
-                float* o = (float*)a.y + at;
-                if (vec) {
-                    if (lo_ok) *reinterpret_cast<float2*>(o) = make_float2(y[0], y[1]);
-                } else {
-                    if (lo_ok) o[0] = y[0];
-                    if (hi_ok) o[1] = y[1];
+                if (VEC) *reinterpret_cast<f2*>(o) = y;
+                else {
+                    reinterpret_cast<float*>(o)[0] = lo;
+                    if (hi_ok) reinterpret_cast<float*>(o)[1] = hi;
                 }
             } else {
-                __nv_bfloat16* o = (__nv_bfloat16*)a.y + at;
-                if (vec) {
-                    if (lo_ok)
-                        *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(y[0], y[1]);
-                } else {
-                    if (lo_ok) o[0] = __float2bfloat16_rn(y[0]);
-                    if (hi_ok) o[1] = __float2bfloat16_rn(y[1]);
+                if (VEC) *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(lo, hi);
+                else {
+                    reinterpret_cast<__nv_bfloat16*>(o)[0] = __float2bfloat16_rn(lo);
+                    if (hi_ok) reinterpret_cast<__nv_bfloat16*>(o)[1] = __float2bfloat16_rn(hi);
                 }
             }
         }
@@ -285,18 +331,18 @@ __device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p,
     if (p.t0 < p.t1) load(rmax);
 #pragma unroll 1
     for (long long t = p.t0; t < p.t1; t += TT, turn ^= 1) {
-        ScanTile<K>& w = tiles[turn];
+        Tile& w = tiles[turn];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            if (MODE == 0) pu[e] = cu[e], pz[e] = cz[e], cz[e] = rz[e];
-            cu[e] = ru[e];
             const int row = prow + e * RP;
-            float x = rd[e].lo() + bias[0], y = rd[e].hi() + bias[1];
-            if (a.in.softplus) softplus2(x, y);
-            float xu = x * cu[e].lo(), yu = y * cu[e].hi();
-            if (row > rmax) x = y = xu = yu = 0.f;  // decay 1, nothing added
-            w.dtu[row][2 * pr] = make_ulonglong2(pack(x, x), pack(xu, xu));
-            w.dtu[row][2 * pr + 1] = make_ulonglong2(pack(y, y), pack(yu, yu));
+            f2 dt = add2(rd[e].get(), bias);
+            if (a.in.softplus) dt = softplus2(dt);
+            f2 du = mul2(dt, ru[e].get());
+            if (row > rmax) dt = du = pack(0.f, 0.f);  // decay 1, nothing added
+            float4 v;
+            unpack(dt, v.x, v.z);
+            unpack(du, v.y, v.w);
+            if (TT % RP == 0 || row < TT) w.dt[row][pr] = v;
         }
 #pragma unroll
         for (int e = 0; e < EB; ++e) {
@@ -306,30 +352,41 @@ __device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p,
                 if (MODE == 0) w.c[row][bm] = bm_ok && row <= rmax ? to_f32(rC[e]) : 0.f;
             }
         }
-        bar_arrive(1 + turn);
+        bar_arrive<NT + SV>(1 + turn);
+        // The scan is done with the other set: it may be stored and filled again.
+        if (t > p.t0) {
+            bar_sync<NT + SV>(3 + (turn ^ 1));
+            if (MODE == 0) finish(t - TT, tiles[turn ^ 1]);
+        }
+        if (MODE == 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) pu[e] = ru[e], pz[e] = rz[e];
+        }
         if (t + TT < p.t1) {
             rmax = (int)(p.t1 - t - TT < TT ? p.t1 - t - TT : TT) - 1;
             load(rmax);
         }
-        // The scan is done with the other set: it may be stored and filled again.
-        if (t > p.t0) {
-            bar_sync(3 + (turn ^ 1));
-            if (MODE == 0) finish(t - TT, tiles[turn ^ 1]);
-        }
     }
     if (p.t0 < p.t1) {
         const int final_turn = turn ^ 1;
-        bar_sync(3 + final_turn);
-        if (MODE == 0) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) pu[e] = cu[e], pz[e] = cz[e];
-            finish(p.t0 + (p.t1 - p.t0 - 1) / TT * TT, tiles[final_turn]);
-        }
+        bar_sync<NT + SV>(3 + final_turn);
+        if (MODE == 0) finish(p.t0 + (p.t1 - p.t0 - 1) / TT * TT, tiles[final_turn]);
     }
 }
 
-template <typename T, int K, int MODE>
-__global__ void __launch_bounds__(2 * NT, 2) scan_kernel(ScanArgs a)
+// MODE 0: with outputs. MODE 1: the chunks' states only.
+//
+// The CTA's first NT threads scan, the other SV serve them, tile by tile of TT
+// tokens through two sets of shared buffers. The servers turn pairs of channels
+// into dt and dt u; the scanning threads carry four states of two channels each
+// over the tile and leave their shares of C . h; the servers add the K shares,
+// the skip and the gate and store. So the exponentials of the scan run while the
+// next tile is made and the last one stored. Two channels per thread, because
+// what a thread reads from shared memory per token (B, C and its dt, dt u, a
+// wavefront per word whether other lanes read the same word or not) otherwise
+// takes longer than its exponentials: with one channel, 8K x 8192 took 681 us.
+template <typename T, int K, int MODE, bool VEC, int SV>
+__global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     ScanTile<K>* tiles = reinterpret_cast<ScanTile<K>*>(smem);
@@ -347,8 +404,8 @@ __global__ void __launch_bounds__(2 * NT, 2) scan_kernel(ScanArgs a)
     p.g = cb / a.cpg;
     p.c0 = p.g * Dg + (cb % a.cpg) * ScanTile<K>::CC;
     p.c_end = (p.g + 1) * Dg;
-    if (threadIdx.x < NT) scan_threads<K, MODE>(a, p, tiles);
-    else if (MODE == 0 || p.chunk < p.nchunks - 1) serve_threads<T, K, MODE>(a, p, tiles);
+    if (threadIdx.x < NT) scan_threads<K, MODE, SV>(a, p, tiles);
+    else if (MODE == 0 || p.chunk < p.nchunks - 1) serve_threads<T, K, MODE, VEC, SV>(a, p, tiles);
 }
 
 // One token per sequence: the states are the traffic, one vector of four per
@@ -439,23 +496,23 @@ __global__ void __launch_bounds__(1024) plan_chunks_kernel(SeqView v, long long 
     }
 }
 
+constexpr int SMS = 148;
+
 struct ForwardPlan {
     long long len;  // tokens per chunk, 0: one chunk per sequence
     int items;
 };
 
-// How the forward scan is cut. One warp on each of the GPU's 592 schedulers is
-// what a scan should have at least; chunks are made for two. A packed batch's
-// lengths are not known here, so that it counts as one long sequence: where its
-// sequences are shorter than a chunk, the first launch finds nothing to do.
+// How the forward scan is cut. A packed batch's lengths are not known here, so
+// that it counts as one long sequence: where its sequences are shorter than a
+// chunk, the first launch finds nothing to do.
 ForwardPlan plan_forward(bool packed, int G, int D, long long total, int n, int num_seqs)
 {
-    constexpr long long SCHEDULERS = 148 * 4;
-    const int K = scan_lanes(n), CC = NT / K;
-    const long long warps = (long long)G * ((D / G + CC - 1) / CC) * (NT / 32);
-    if (num_seqs == 0 || total == 0 || (packed ? 1 : num_seqs) * warps >= SCHEDULERS)
+    const int CC = 2 * NT / scan_lanes(n);
+    const long long ctas = (long long)G * ((D / G + CC - 1) / CC);
+    if (num_seqs == 0 || total == 0 || (packed ? 1 : num_seqs) * ctas * 2 > SMS)
         return {0, num_seqs};
-    long long want = (2 * SCHEDULERS + warps - 1) / warps;  // chunks in all
+    long long want = 2 * SMS / ctas;  // chunks in all: two CTAs per SM
     if (want > 64) want = 64;
     long long len = ((total + want - 1) / want + 31) / 32 * 32;
     if (len < 64) len = 64;
@@ -464,18 +521,18 @@ ForwardPlan plan_forward(bool packed, int G, int D, long long total, int n, int 
     return {len, (int)(total / len + num_seqs)};
 }
 
-// The pass over the chunks' states (if any) and the pass with outputs.
-template <int K>
+// The pass over the chunks' states (when cut) and the pass with outputs.
+template <int K, int SV>
 cudaError_t launch_tiles(void (*states)(ScanArgs), void (*outputs)(ScanArgs), const ScanArgs& a,
-                         unsigned grid, cudaStream_t stream)
+                         bool cut, unsigned grid, cudaStream_t stream)
 {
     constexpr int smem = 2 * (int)sizeof(ScanTile<K>);
-    for (auto kernel : {states, outputs}) {
+    for (auto kernel : {cut ? states : nullptr, outputs}) {
         if (!kernel) continue;
         cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kernel<<<grid, 2 * NT, smem, stream>>>(a);
+        kernel<<<grid, NT + SV, smem, stream>>>(a);
         count_launch();
     }
     return cudaGetLastError();
@@ -506,7 +563,7 @@ size_t scan_workspace(bool backward, int G, int D, long long total, int n, int n
 cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, float* state_out,
                         void* ws, cudaStream_t stream)
 {
-    const int K = scan_lanes(p.n), CC = NT / K, Dg = p.D / p.G;
+    const int K = scan_lanes(p.n), CC = 2 * NT / K, Dg = p.D / p.G;
     ScanArgs a{};
     a.in = p.in;
     a.view = p.view;
@@ -522,8 +579,8 @@ cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, fl
     const auto pairs = [&](const void* q, long long ld) {
         return (uintptr_t)q % two == 0 && ld % 2 == 0;
     };
-    a.vec = Dg % 2 == 0 && pairs(p.in.u, p.in.ld_u) && pairs(p.in.delta, p.in.ld_delta) &&
-            (!p.in.z || pairs(p.in.z, p.in.ld_z));
+    const bool vec = Dg % 2 == 0 && pairs(p.in.u, p.in.ld_u) && pairs(p.in.delta, p.in.ld_delta) &&
+                     (!p.in.z || pairs(p.in.z, p.in.ld_z));
     const ForwardPlan f = plan_forward(p.view.cu != nullptr, p.G, p.D, p.view.total, p.n,
                                        p.view.num_seqs);
     a.ch.len = LLONG_MAX / 2;
@@ -551,17 +608,22 @@ cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, fl
     }
     const unsigned grid = (unsigned)((long long)a.ch.items * a.G * a.cpg);
     cudaError_t e = cudaSuccess;
+#define LA_TYPE(T, KK)                                                                           \
+    if (!vec)                                                                                    \
+        e = launch_tiles<KK, 256>(scan_kernel<T, KK, 1, false, 256>,                             \
+                                  scan_kernel<T, KK, 0, false, 256>, a, f.len != 0, grid, stream); \
+    else if (grid <= SMS)                                                                        \
+        e = launch_tiles<KK, 512>(scan_kernel<T, KK, 1, true, 512>,                              \
+                                  scan_kernel<T, KK, 0, true, 512>, a, f.len != 0, grid, stream); \
+    else                                                                                         \
+        e = launch_tiles<KK, 256>(scan_kernel<T, KK, 1, true, 256>,                              \
+                                  scan_kernel<T, KK, 0, true, 256>, a, f.len != 0, grid, stream)
 #define LA_CALL(KK)                                                                              \
-    do {                                                                                         \
-        const bool low = p.in_t == LA_BF16;                                                      \
-        e = launch_tiles<KK>(f.len ? (low ? scan_kernel<__nv_bfloat16, KK, 1>                    \
-                                          : scan_kernel<float, KK, 1>)                           \
-                                   : nullptr,                                                    \
-                             low ? scan_kernel<__nv_bfloat16, KK, 0> : scan_kernel<float, KK, 0>, \
-                             a, grid, stream);                                                   \
-    } while (0)
+    if (p.in_t == LA_BF16) { LA_TYPE(__nv_bfloat16, KK); }                                       \
+    else { LA_TYPE(float, KK); }
     LA_SCAN_DISPATCH_K(p.n, LA_CALL)
 #undef LA_CALL
+#undef LA_TYPE
     return e;
 }
 

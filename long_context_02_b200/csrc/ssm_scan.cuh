@@ -75,56 +75,72 @@ __device__ __forceinline__ float sigmoid_f(float x)
 }
 
 // exp(-|x|): the product |x| log2 e is rounded to fp32, an error of up to
-// 2^-24 |x| log2 e in the exponent; its rest, from one multiply-add more, is put
+// 2^-24 |x| log2 e in the exponent; its rest, from two multiply-adds more, is put
 // back by a first-order factor. Beyond 100 the result counts as e^-100, which
-// spares the case of an infinite product (and a NaN stays one).
-__device__ __forceinline__ float exp_neg_abs(float x)
+// spares the case of an infinite product.
+__device__ __forceinline__ f2 exp_neg_abs2(float x, float y)
 {
     constexpr float LO = 1.9259629e-8f;  // log2 e - fp32(log2 e)
-    float t = fabsf(x);
-    t = t > 100.f ? 100.f : t;
-    const float hi = -SCAN_LOG2E * t;
-    const float lo = fmaf(-LO, t, fmaf(-SCAN_LOG2E, t, -hi));
-    const float e = ex2(hi);
-    return fmaf(e, lo * SCAN_LN2, e);
+    const f2 t = pack(fminf(fabsf(x), 100.f), fminf(fabsf(y), 100.f));
+    const f2 c = pack(-SCAN_LOG2E, -SCAN_LOG2E);
+    const f2 hi = mul2(t, c);
+    const f2 lo = fma2(t, pack(-LO, -LO), fma2(t, c, mul2(hi, pack(-1.f, -1.f))));
+    const f2 e = ex2_2(hi);
+    return fma2(mul2(e, lo), pack(SCAN_LN2, SCAN_LN2), e);
+}
+__device__ __forceinline__ float exp_neg_abs(float x)
+{
+    float a, b;
+    unpack(exp_neg_abs2(x, 0.f), a, b);
+    return a;
+}
+// max(x, 0), NaN for NaN.
+__device__ __forceinline__ float relu_nan(float x)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) <= 1. The logarithm by
-// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, and the series of atanh: its
-// terms are positive, so small results keep their relative precision (the
-// first term left out is below 2^-25 of the sum). Its derivative, sigmoid(x),
-// is 1 / (1 + e) or e / (1 + e).
-__device__ __forceinline__ f2 atanh_series(f2 q)
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, which keeps the relative
+// precision of small results. atanh(s) / s is a polynomial in q = s^2 <= 1/9,
+// the minimax one of degree 4 (Remez exchange; its error is 4.1e-9). The
+// derivative, sigmoid(x), is 1 / (1 + e) or e / (1 + e).
+__device__ __forceinline__ f2 atanh_ratio(f2 q)
 {
-    f2 p = pack(1.f / 15, 1.f / 15);
-    p = fma2(p, q, pack(1.f / 13, 1.f / 13));
-    p = fma2(p, q, pack(1.f / 11, 1.f / 11));
-    p = fma2(p, q, pack(1.f / 9, 1.f / 9));
-    p = fma2(p, q, pack(1.f / 7, 1.f / 7));
-    p = fma2(p, q, pack(1.f / 5, 1.f / 5));
-    p = fma2(p, q, pack(1.f / 3, 1.f / 3));
+    f2 p = fma2(q, pack(0.14095774f, 0.14095774f), pack(0.13978833f, 0.13978833f));
+    p = fma2(p, q, pack(0.20012558f, 0.20012558f));
+    p = fma2(p, q, pack(0.33333156f, 0.33333156f));
     return fma2(p, q, pack(1.f, 1.f));
 }
-__device__ __forceinline__ void softplus2(float& x, float& y)
+__device__ __forceinline__ f2 softplus2(f2 v)
 {
-    const float ex = exp_neg_abs(x), ey = exp_neg_abs(y);
-    const f2 s = mul2(pack(ex, ey), pack(rcp(2.f + ex), rcp(2.f + ey)));
-    float px, py;
-    unpack(mul2(s, atanh_series(mul2(s, s))), px, py);
-    x = fmaf(2.f, px, fmaxf(x, 0.f));
-    y = fmaf(2.f, py, fmaxf(y, 0.f));
+    float x, y, a, b;
+    unpack(v, x, y);
+    const f2 e = exp_neg_abs2(x, y);
+    unpack(add2(e, pack(2.f, 2.f)), a, b);
+    const f2 s = mul2(e, pack(rcp(a), rcp(b)));
+    return fma2(mul2(s, pack(2.f, 2.f)), atanh_ratio(mul2(s, s)),
+                pack(relu_nan(x), relu_nan(y)));
 }
 __device__ __forceinline__ float softplus_f(float x)
 {
-    float y = 0.f;
-    softplus2(x, y);
-    return x;
+    float y, unused;
+    unpack(softplus2(pack(x, 0.f)), y, unused);
+    return y;
+}
+__device__ __forceinline__ f2 sigmoid2(f2 x)
+{
+    float a, b;
+    unpack(add2(ex2_2(mul2(x, pack(-SCAN_LOG2E, -SCAN_LOG2E))), pack(1.f, 1.f)), a, b);
+    return pack(rcp(a), rcp(b));
 }
 // softplus and its derivative.
 __device__ __forceinline__ float softplus_slope(float x)
 {
     const float e = exp_neg_abs(x), r = rcp(1.f + e);
-    return x >= 0.f ? r : e * r;
+    return x >= 0.f ? r : x < 0.f ? e * r : x;  // NaN for NaN
 }
 
 // Sum V values over the M lanes that differ in the bits [STEP, STEP M) of the
