@@ -37,32 +37,6 @@ struct ScanArgs {
     int out_f32;
 };
 
-// Two adjacent channels of a token as loaded: one access where VEC (every row
-// of every tensor then starts on such a pair), else two.
-template <typename T, bool VEC> struct Pair;
-template <bool VEC> struct Pair<__nv_bfloat16, VEC> {
-    uint32_t w;
-    __device__ __forceinline__ void load(const char* p, uint32_t next)
-    {
-        if (VEC) w = *reinterpret_cast<const uint32_t*>(p);
-        else w = *reinterpret_cast<const uint16_t*>(p) |
-                 (uint32_t) * reinterpret_cast<const uint16_t*>(p + next) << 16;
-    }
-    __device__ __forceinline__ f2 get() const
-    {
-        return pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    }
-};
-template <bool VEC> struct Pair<float, VEC> {
-    f2 v;
-    __device__ __forceinline__ void load(const char* p, uint32_t next)
-    {
-        if (VEC) v = *reinterpret_cast<const f2*>(p);
-        else v = pack(*reinterpret_cast<const float*>(p), *reinterpret_cast<const float*>(p + next));
-    }
-    __device__ __forceinline__ f2 get() const { return v; }
-};
-
 // Named barriers of a CTA: `arrive` counts this warp in without waiting.
 template <int THREADS> __device__ __forceinline__ void bar_sync(int id)
 {

@@ -136,11 +136,17 @@ __device__ __forceinline__ f2 sigmoid2(f2 x)
     unpack(add2(ex2_2(mul2(x, pack(-SCAN_LOG2E, -SCAN_LOG2E))), pack(1.f, 1.f)), a, b);
     return pack(rcp(a), rcp(b));
 }
-// softplus and its derivative.
-__device__ __forceinline__ float softplus_slope(float x)
+// The derivative of softplus.
+__device__ __forceinline__ f2 softplus_slope2(f2 v)
 {
-    const float e = exp_neg_abs(x), r = rcp(1.f + e);
-    return x >= 0.f ? r : x < 0.f ? e * r : x;  // NaN for NaN
+    float x, y, e0, e1, a, b;
+    unpack(v, x, y);
+    const f2 e = exp_neg_abs2(x, y);
+    unpack(e, e0, e1);
+    unpack(add2(e, pack(1.f, 1.f)), a, b);
+    // x < 0: e / (1 + e); NaN: itself
+    return mul2(pack(rcp(a), rcp(b)), pack(x >= 0.f ? 1.f : x < 0.f ? e0 : x,
+                                           y >= 0.f ? 1.f : y < 0.f ? e1 : y));
 }
 
 // Sum V values over the M lanes that differ in the bits [STEP, STEP M) of the
@@ -188,6 +194,32 @@ template <int V, int M, int STEP> __device__ __forceinline__ bool reduced_writer
 {
     return M <= V || (lane & ((M / V - 1) * STEP)) == 0;
 }
+
+// Two adjacent channels of a token as loaded: one access where VEC (every row
+// of every tensor then starts on such a pair), else two.
+template <typename T, bool VEC> struct Pair;
+template <bool VEC> struct Pair<__nv_bfloat16, VEC> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const char* p, uint32_t next)
+    {
+        if (VEC) w = *reinterpret_cast<const uint32_t*>(p);
+        else w = *reinterpret_cast<const uint16_t*>(p) |
+                 (uint32_t) * reinterpret_cast<const uint16_t*>(p + next) << 16;
+    }
+    __device__ __forceinline__ f2 get() const
+    {
+        return pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+};
+template <bool VEC> struct Pair<float, VEC> {
+    f2 v;
+    __device__ __forceinline__ void load(const char* p, uint32_t next)
+    {
+        if (VEC) v = *reinterpret_cast<const f2*>(p);
+        else v = pack(*reinterpret_cast<const float*>(p), *reinterpret_cast<const float*>(p + next));
+    }
+    __device__ __forceinline__ f2 get() const { return v; }
+};
 
 // Four states of one channel at p (n of them in all, this thread's start at
 // m0); vectors when a row of n states keeps 16-byte alignment.

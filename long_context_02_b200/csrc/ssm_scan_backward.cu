@@ -1,21 +1,24 @@
 // Gradients of the selective scan (formulas in lightning.h).
 //
 // The sequences are cut into chunks of LEN tokens, all of them independent:
-//  1. local pass: each chunk's state from zero, h_c; the sum of its dt, whose
-//     exponential exp(A sum dt) is the chunk's whole decay; and the gradient
-//     that the chunk's own outputs send to the state before it,
+//  1. local pass: each chunk's state from zero, h_c, and that state before every
+//     block of 8 tokens; the sums of dt to the same places, whose exponentials
+//     exp(A sum dt) are the decays from the chunk's start; and the gradient that
+//     the chunk's own outputs send to the state before it,
 //     G_c = sum_t (prod_{s<=t} a_s) C_t dyz_t.
 //  2. combine: forward over the chunks, the state before each; backward over
 //     them, the gradient of the state after each (from dstate_out).
-//  3. main pass: per chunk, a forward walk that leaves the state before every
-//     block of 8 tokens in shared memory, then the blocks from the last to the
-//     first: forward again with the 8 states and decays in registers, and the
-//     reverse recurrence over them. The exponentials are thus taken three times
-//     (once per walk), which costs less than moving states or decays through
-//     shared memory.
+//  3. main pass: the blocks of a chunk from the last to the first. The state
+//     before a block is its local part plus the decayed state before the chunk;
+//     a forward walk over the 8 tokens keeps their states in registers, a
+//     reverse walk carries the gradient. The exponentials are taken once per
+//     walk, three times in all.
 //  4. reductions of dB and dC over the channel blocks and of dA, dD and
 //     ddelta_bias over the chunks, from partial sums in the workspace, in a
 //     fixed order.
+// As in the forward scan a thread holds four states of two channels: what it
+// reads from shared memory per token, and the sums over channels (shuffles take
+// the same path), would otherwise take longer than the exponentials.
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -24,9 +27,8 @@ namespace la {
 namespace {
 
 constexpr int LEN = 128;  // tokens per chunk
-constexpr int BLK = 8;    // tokens per block of the main pass
-constexpr int NT1 = 128;  // threads of the local pass
-constexpr int NT3 = 256;  // threads of the main pass
+constexpr int BLK = 8;    // tokens per block
+constexpr int NT = 128;   // threads per CTA of the local and the main pass
 
 struct BackArgs {
     la_scan_inputs in;
@@ -38,6 +40,8 @@ struct BackArgs {
     float* hs;      // [items][D][n]: chunk states, then states before the chunks, then dA partials
     float* gs;      // [items][D][n]: G of the chunks, then gradients of the states after them
     float* dtsum;   // [items][D]
+    float* ck;      // [items][LEN / BLK][D][n]: local state before each block but the first
+    float* ckdt;    // [items][LEN / BLK][D]: sum of the chunk's dt before each block
     float* dDp;     // [items][D]
     float* dbp;     // [items][D]
     float* dBp;     // [cpg][total][G][n]
@@ -46,135 +50,247 @@ struct BackArgs {
     int out_f32;
 };
 
-template <typename T>
-__device__ __forceinline__ void store_out(void* p, long long i, float v, int f32)
-{
-    if (f32) ((float*)p)[i] = v;
-    else ((__nv_bfloat16*)p)[i] = __float2bfloat16_rn(v);
-}
-
 // A CTA's chunk and channels.
 struct Place {
-    int c0, c_end, g, cbg;
+    int item, c0, c_end, g, cbg;
     long long t0, t1;
     // An item of a packed batch's table behind its last chunk gets no tokens.
-    __device__ __forceinline__ Place(const BackArgs& a, int item, int cb, int cpg, int CC)
+    __device__ __forceinline__ Place(const BackArgs& a, int CC)
     {
-        const int s = a.ch.seq(item), Dg = a.D / a.G;
+        const int blocks = a.G * a.cpg, cb = blockIdx.x % blocks, Dg = a.D / a.G;
+        item = blockIdx.x / blocks;
+        const int s = a.ch.seq(item);
         t0 = t1 = 0;
         if (s >= 0) {
             a.view.range(s, t0, t1);
             t0 += (item - a.ch.first_of(s)) * a.ch.len;
             if (t1 - t0 > a.ch.len) t1 = t0 + a.ch.len;
         }
-        g = cb / cpg;
-        cbg = cb % cpg;
+        g = cb / a.cpg;
+        cbg = cb % a.cpg;
         c0 = g * Dg + cbg * CC;
         c_end = (g + 1) * Dg;
     }
 };
 
-template <typename T, int K>
-__global__ void __launch_bounds__(NT1) local_kernel(BackArgs a, int cpg1)
-{
-    constexpr int S = SCAN_S, NP = S * K, CC = NT1 / K;
-    constexpr int TT = K == 1 ? 8 : K == 2 || K == 16 ? 16 : 32;
-    constexpr int E = TT * CC / NT1;
-    constexpr int EB = (TT * NP + NT1 - 1) / NT1;
-    __shared__ float2 dtu[TT][CC];
-    __shared__ float dyz[TT][CC];
-    __shared__ __align__(16) float bc[2][TT][NP];
+// The token inputs of a CTA, block by block of BLK tokens: each thread holds E
+// pairs of channels and EB values of B and of C. Addresses are a base that all
+// threads share and a thread's own 32-bit offset from it.
+template <typename T, int K, bool VEC> struct Inputs {
+    static constexpr int NP = SCAN_S * K, CC = 2 * NT / K, CP = CC / 2;
+    static constexpr int RP = NT / CP;                        // rows between a thread's pairs
+    static constexpr int E = (BLK + RP - 1) / RP;
+    static constexpr int RB = NT / NP, EB = (BLK + RB - 1) / RB;
+    static constexpr uint32_t TS = sizeof(T);
+    Pair<T, VEC> u[E], d[E], z[E], y[E];
+    T B[EB], C[EB];
+    const char *up, *dp, *zp, *yp, *Bp, *Cp;
+    uint32_t lu, ld, lz, ly, lb, lc, ch_at, bm_at, next;
+    int prow, brow;
+    bool gated, lo_ok, hi_ok;  // whether the pair's channels are the CTA's
 
-    const int tid = threadIdx.x;
-    const int blocks = a.G * cpg1;
-    const int item = blockIdx.x / blocks;
-    const Place p(a, item, blockIdx.x % blocks, cpg1, CC);
-    const int sch = tid / K, m0 = (tid % K) * S, sc = p.c0 + sch;
-    const bool sc_ok = sc < p.c_end;
-    const int ech = tid % CC, etok = tid / CC, ec = p.c0 + ech;
-    const bool ec_ok = ec < p.c_end;
-
-    float A2[S] = {0.f, 0.f, 0.f, 0.f};
-    if (sc_ok) load_states(A2, a.in.A + (long long)sc * a.n, m0, a.n);
-    float h[S], G[S], P[S], dts = 0.f;
-#pragma unroll
-    for (int i = 0; i < S; ++i) A2[i] *= SCAN_LOG2E, h[i] = G[i] = 0.f, P[i] = 1.f;
-
-    const T* up = (const T*)a.in.u + ec;
-    const T* dp = (const T*)a.in.delta + ec;
-    const T* zp = a.in.z ? (const T*)a.in.z + ec : nullptr;
-    const T* yp = (const T*)a.dy + ec;
-    const T* Bp = (const T*)a.in.B + (long long)p.g * a.n;
-    const T* Cp = (const T*)a.in.C + (long long)p.g * a.n;
-    const float dbias = a.in.delta_bias && ec_ok ? a.in.delta_bias[ec] : 0.f;
-    const long long t1 = p.t1;
-
-    T ru[E], rd[E], rz[E], ry[E], rB[EB], rC[EB];
-    auto load = [&](long long t) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const long long tok = t + e * K + etok;
-            const bool ok = ec_ok && tok < t1;
-            ru[e] = ok ? up[tok * a.in.ld_u] : T(0.f);
-            rd[e] = ok ? dp[tok * a.in.ld_delta] : T(0.f);
-            ry[e] = ok ? yp[tok * a.ld_dy] : T(0.f);
-            rz[e] = ok && zp ? zp[tok * a.in.ld_z] : T(0.f);
-        }
-#pragma unroll
-        for (int e = 0; e < EB; ++e) {
-            const int idx = e * NT1 + tid, m = idx % NP;
-            const long long tok = t + idx / NP;
-            const bool ok = m < a.n && tok < t1 && idx < TT * NP;
-            rB[e] = ok ? Bp[tok * a.in.ld_b + m] : T(0.f);
-            rC[e] = ok ? Cp[tok * a.in.ld_c + m] : T(0.f);
-        }
-    };
-    if (p.t0 < t1) load(p.t0);
-    for (long long t = p.t0; t < t1; t += TT) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            float dt = to_f32(rd[e]) + dbias;
-            if (a.in.softplus) dt = softplus_f(dt);
-            if (!ec_ok || t + e * K + etok >= t1) dt = 0.f;
-            dtu[e * K + etok][ech] = make_float2(dt, dt * to_f32(ru[e]));
-            float y = to_f32(ry[e]);
-            const float z = to_f32(rz[e]);
-            if (zp) y *= z * sigmoid_f(z);
-            dyz[e * K + etok][ech] = y;
-        }
-#pragma unroll
-        for (int e = 0; e < EB; ++e) {
-            const int idx = e * NT1 + tid;
-            if (idx < TT * NP) {
-                (&bc[0][0][0])[idx] = to_f32(rB[e]);
-                (&bc[1][0][0])[idx] = to_f32(rC[e]);
-            }
-        }
-        __syncthreads();
-        if (t + TT < t1) load(t + TT);
-#pragma unroll 8
-        for (int q = 0; q < TT; ++q) {
-            const float2 d = dtu[q][sch];
-            const float w = dyz[q][sch];
-            const float4 b4 = *reinterpret_cast<const float4*>(&bc[0][q][m0]);
-            const float4 c4 = *reinterpret_cast<const float4*>(&bc[1][q][m0]);
-            const float bv[S] = {b4.x, b4.y, b4.z, b4.w}, cv[S] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                const float e = ex2(d.x * A2[i]);
-                h[i] = fmaf(e, h[i], d.y * bv[i]);
-                P[i] *= e;
-                G[i] = fmaf(P[i], w * cv[i], G[i]);
-            }
-            dts += d.x;
-        }
-        __syncthreads();
+    __device__ __forceinline__ Inputs(const BackArgs& a, const Place& p)
+    {
+        const int tid = threadIdx.x, pr = tid % CP, ec = p.c0 + 2 * pr;
+        lo_ok = ec < p.c_end;
+        hi_ok = ec + 1 < p.c_end;
+        // Channels behind the group's last read the last ones.
+        const int ch = lo_ok ? 2 * pr : p.c_end - p.c0 - (VEC ? 2 : 1);
+        const int bm = tid % NP;
+        prow = tid / CP;
+        brow = tid / NP;
+        next = hi_ok ? TS : 0;
+        ch_at = ch * TS;
+        bm_at = (bm < a.n ? bm : 0) * TS;
+        lu = (uint32_t)a.in.ld_u * TS;
+        ld = (uint32_t)a.in.ld_delta * TS;
+        lz = (uint32_t)a.in.ld_z * TS;
+        ly = (uint32_t)a.ld_dy * TS;
+        lb = (uint32_t)a.in.ld_b * TS;
+        lc = (uint32_t)a.in.ld_c * TS;
+        up = (const char*)a.in.u + ((long long)p.c0 + p.t0 * a.in.ld_u) * TS;
+        dp = (const char*)a.in.delta + ((long long)p.c0 + p.t0 * a.in.ld_delta) * TS;
+        zp = (const char*)a.in.z + ((long long)p.c0 + p.t0 * a.in.ld_z) * TS;
+        yp = (const char*)a.dy + ((long long)p.c0 + p.t0 * a.ld_dy) * TS;
+        Bp = (const char*)a.in.B + ((long long)p.g * a.n + p.t0 * a.in.ld_b) * TS;
+        Cp = (const char*)a.in.C + ((long long)p.g * a.n + p.t0 * a.in.ld_c) * TS;
+        gated = a.in.z != nullptr;
     }
-    if (!sc_ok) return;
-    const long long slot = (long long)item * a.D + sc;
-    store_states(a.hs + slot * a.n, h, m0, a.n);
-    store_states(a.gs + slot * a.n, G, m0, a.n);
-    if (m0 == 0) a.dtsum[slot] = dts;
+    // Block blk of the chunk; rows behind rmax (counted from the block's first) read that one.
+    __device__ __forceinline__ void load(int blk, int rmax)
+    {
+        const long long r = (long long)blk * BLK;
+        const char *u_ = up + r * lu, *d_ = dp + r * ld, *z_ = zp + r * lz, *y_ = yp + r * ly;
+        const char *B_ = Bp + r * lb, *C_ = Cp + r * lc;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t row = min(prow + e * RP, rmax);
+            u[e].load(u_ + (row * lu + ch_at), next);
+            d[e].load(d_ + (row * ld + ch_at), next);
+            y[e].load(y_ + (row * ly + ch_at), next);
+            if (gated) z[e].load(z_ + (row * lz + ch_at), next);
+        }
+#pragma unroll
+        for (int e = 0; e < EB; ++e) {
+            const uint32_t row = min(brow + e * RB, rmax);
+            B[e] = *reinterpret_cast<const T*>(B_ + (row * lb + bm_at));
+            C[e] = *reinterpret_cast<const T*>(C_ + (row * lc + bm_at));
+        }
+    }
+};
+
+// A block's inputs as the scanning threads read them.
+template <int K> struct Block {
+    static constexpr int NP = SCAN_S * K, CP = NT / K;
+    float4 dt[BLK][CP];  // dt, dt u of the pair's first channel, then of its second
+    f2 w[BLK][CP];       // dy times the gate
+    float b[BLK][NP];
+    float c[BLK][NP];
+};
+
+template <typename T, int K, bool VEC>
+__device__ __forceinline__ void fill_block(Block<K>& blk, const Inputs<T, K, VEC>& in, int n,
+                                           int rmax, f2 bias, bool softplus)
+{
+    using I = Inputs<T, K, VEC>;
+    const int pr = threadIdx.x % I::CP, bm = threadIdx.x % I::NP;
+#pragma unroll
+    for (int e = 0; e < I::E; ++e) {
+        const int row = in.prow + e * I::RP;
+        if (BLK % I::RP && row >= BLK) continue;
+        f2 dt = add2(in.d[e].get(), bias), w = in.y[e].get();
+        if (softplus) dt = softplus2(dt);
+        f2 du = mul2(dt, in.u[e].get());
+        if (in.gated) {
+            const f2 z = in.z[e].get();
+            w = mul2(w, mul2(z, sigmoid2(z)));
+        }
+        if (row > rmax || !in.lo_ok) dt = du = w = pack(0.f, 0.f);  // decay 1, nothing added
+        if (!in.hi_ok) {  // a channel of the next group adds nothing to this one's sums
+            float lo, hi;
+            unpack(du, lo, hi);
+            du = pack(lo, 0.f);
+            unpack(w, lo, hi);
+            w = pack(lo, 0.f);
+        }
+        float4 v;
+        unpack(dt, v.x, v.z);
+        unpack(du, v.y, v.w);
+        blk.dt[row][pr] = v;
+        blk.w[row][pr] = w;
+    }
+#pragma unroll
+    for (int e = 0; e < I::EB; ++e) {
+        const int row = in.brow + e * I::RB;
+        if (BLK % I::RB && row >= BLK) continue;
+        const bool ok = bm < n && row <= rmax;
+        blk.b[row][bm] = ok ? to_f32(in.B[e]) : 0.f;
+        blk.c[row][bm] = ok ? to_f32(in.C[e]) : 0.f;
+    }
+}
+
+// A pair of channels' values of a [D] vector; zeros where there are none.
+__device__ __forceinline__ f2 channel_pair(const float* v, int c, int c_end)
+{
+    return pack(v && c < c_end ? v[c] : 0.f, v && c + 1 < c_end ? v[c + 1] : 0.f);
+}
+
+// -A log2 e etc. of a thread's four states of two channels.
+__device__ __forceinline__ void load_decays(f2 (*A)[2], const BackArgs& a, int c, int c_end, int m0)
+{
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (c + x < c_end) load_states(v, a.in.A + (long long)(c + x) * a.n, m0, a.n);
+        A[x][0] = pack(v[0] * SCAN_LOG2E, v[1] * SCAN_LOG2E);
+        A[x][1] = pack(v[2] * SCAN_LOG2E, v[3] * SCAN_LOG2E);
+    }
+}
+__device__ __forceinline__ void load_pair(f2 (*v)[2], const float* p, const BackArgs& a,
+                                          long long row, int c, int c_end, int m0)
+{
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        if (c + x < c_end) load_states(s, p + (row * a.D + c + x) * a.n, m0, a.n);
+        v[x][0] = pack(s[0], s[1]);
+        v[x][1] = pack(s[2], s[3]);
+    }
+}
+__device__ __forceinline__ void store_pair(float* p, f2 (*v)[2], const BackArgs& a, long long row,
+                                           int c, int c_end, int m0)
+{
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        float s[4];
+        unpack(v[x][0], s[0], s[1]);
+        unpack(v[x][1], s[2], s[3]);
+        if (c + x < c_end) store_states(p + (row * a.D + c + x) * a.n, s, m0, a.n);
+    }
+}
+
+template <typename T, int K, bool VEC>
+__global__ void __launch_bounds__(NT, 4) local_kernel(BackArgs a)
+{
+    using I = Inputs<T, K, VEC>;
+    __shared__ Block<K> blocks[2];
+    const Place p(a, I::CC);
+    const int tid = threadIdx.x, pr = tid / K, m0 = (tid % K) * SCAN_S, c = p.c0 + 2 * pr;
+    f2 A[2][2], h[2][2], G[2][2], P[2][2], dts = pack(0.f, 0.f);
+    load_decays(A, a, c, p.c_end, m0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) h[x][i] = G[x][i] = pack(0.f, 0.f), P[x][i] = pack(1.f, 1.f);
+    I in(a, p);
+    const f2 bias = channel_pair(a.in.delta_bias, p.c0 + 2 * (tid % I::CP), p.c_end);
+    const int len = (int)(p.t1 - p.t0), nblk = (len + BLK - 1) / BLK;
+    if (nblk > 0) in.load(0, min(BLK, len) - 1);
+#pragma unroll 1
+    for (int b = 0; b < nblk; ++b) {
+        Block<K>& blk = blocks[b & 1];
+        fill_block<T, K, VEC>(blk, in, a.n, min(BLK, len - b * BLK) - 1, bias, a.in.softplus);
+        __syncthreads();
+        if (b + 1 < nblk) in.load(b + 1, min(BLK, len - (b + 1) * BLK) - 1);
+        if (b > 0) {
+            const long long at = (long long)p.item * (LEN / BLK) + b;
+            store_pair(a.ck, h, a, at, c, p.c_end, m0);
+            if (m0 == 0) {
+                float d0, d1;
+                unpack(dts, d0, d1);
+                if (c < p.c_end) a.ckdt[at * a.D + c] = d0;
+                if (c + 1 < p.c_end) a.ckdt[at * a.D + c + 1] = d1;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < BLK; ++q) {
+            const float4 d = blk.dt[q][pr];
+            float w[2];
+            unpack(blk.w[q][pr], w[0], w[1]);
+            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&blk.b[q][m0]);
+            const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&blk.c[q][m0]);
+            const float dt[2] = {d.x, d.z}, du[2] = {d.y, d.w};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const f2 e = ex2_2(mul2(pack(dt[x], dt[x]), A[x][i]));
+                    h[x][i] = fma2(e, h[x][i], mul2(pack(du[x], du[x]), i ? bv.y : bv.x));
+                    P[x][i] = mul2(P[x][i], e);
+                    G[x][i] = fma2(P[x][i], mul2(pack(w[x], w[x]), i ? cv.y : cv.x), G[x][i]);
+                }
+            }
+            dts = add2(dts, pack(dt[0], dt[1]));
+        }
+    }
+    store_pair(a.hs, h, a, p.item, c, p.c_end, m0);
+    store_pair(a.gs, G, a, p.item, c, p.c_end, m0);
+    if (m0 == 0) {
+        float d0, d1;
+        unpack(dts, d0, d1);
+        if (c < p.c_end) a.dtsum[(long long)p.item * a.D + c] = d0;
+        if (c + 1 < p.c_end) a.dtsum[(long long)p.item * a.D + c + 1] = d1;
+    }
 }
 
 // One thread per (channel, state) of a sequence.
@@ -209,289 +325,235 @@ __global__ void __launch_bounds__(128) combine_kernel(BackArgs a, const float* s
 }
 
 template <int K> struct MainShared {
-    static constexpr int NP = SCAN_S * K, CC = NT3 / K;
-    static constexpr int TA = K == 1 ? 8 : K == 2 || K == 16 ? 16 : 32;
-    float4 ck[LEN / BLK][NT3];  // states before each block
-    union {
-        struct {
-            float2 dtu[TA][CC];
-            float b[TA][NP];
-        } a;
-        struct {
-            float2 dtu[BLK][CC];
-            float dyz[BLK][CC];
-            float bc[2][BLK][NP];
-            float gB[BLK][CC], gA[BLK][CC], y[BLK][CC];
-            float red[2][NT3 / 32][BLK][NP];  // dB and dC of each warp's channels
-        } b;
-    } u;
+    static constexpr int NP = SCAN_S * K;
+    Block<K> in;
+    // Each scanning thread's share of sum_m g B, of sum_m A log2 e a h g and of
+    // C . h, for both channels.
+    f2 gB[BLK][NT], gA[BLK][NT], y[BLK][NT];
+    float red[NT / 32][BLK][2][NP];  // dB and dC, summed over each warp's channels
 };
 
-template <typename T, int K>
-__global__ void __launch_bounds__(NT3, 2) main_kernel(BackArgs a)
+template <typename T, int K, bool VEC>
+__device__ __forceinline__ void store_two(const BackArgs& a, void* p, long long row, int c, bool hi,
+                                          f2 v)
 {
-    using Sh = MainShared<K>;
-    constexpr int S = SCAN_S, NP = Sh::NP, CC = Sh::CC, TA = Sh::TA;
-    constexpr int EA = TA * CC / NT3, EBA = (TA * NP + NT3 - 1) / NT3;
-    constexpr int E = (BLK * CC + NT3 - 1) / NT3, EB = (BLK * NP + NT3 - 1) / NT3;
-    constexpr int M = 32 / K;                     // channels per warp
-    constexpr int RC = M < 8 ? 8 / M : 1;         // dB, dC values per lane after the reduction
-    constexpr int RK = K < 4 ? 4 / K : 1;
+    float x, y;
+    unpack(v, x, y);
+    const long long at = row * a.D + c;
+    if (a.out_f32) {
+        float* o = (float*)p + at;
+        if (VEC) *reinterpret_cast<f2*>(o) = v;
+        else {
+            o[0] = x;
+            if (hi) o[1] = y;
+        }
+    } else {
+        __nv_bfloat16* o = (__nv_bfloat16*)p + at;
+        if (VEC) *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x, y);
+        else {
+            o[0] = __float2bfloat16_rn(x);
+            if (hi) o[1] = __float2bfloat16_rn(y);
+        }
+    }
+}
+
+// ex2 that the compiler does not replace by the result of an earlier one: 64
+// decays kept from the forward walk would not fit in registers.
+__device__ __forceinline__ float ex2_again(float x)
+{
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Sum of the K shares of a pair of channels.
+template <int K> __device__ __forceinline__ f2 sum_shares(const f2* v)
+{
+    f2 s;
+#pragma unroll
+    for (int k = 0; k < K; k += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(v + k);
+        s = k ? add2(s, add2(x.x, x.y)) : add2(x.x, x.y);
+    }
+    return s;
+}
+
+template <typename T, int K, bool VEC>
+__global__ void __launch_bounds__(NT, 3) main_kernel(BackArgs a)
+{
+    using I = Inputs<T, K, VEC>;
+    constexpr int S = SCAN_S, NP = I::NP, M = 32 / K;  // M: pairs of channels per warp
+    constexpr int RC = M < 8 ? 8 / M : 1;              // dB, dC values per lane when reduced
     extern __shared__ __align__(16) unsigned char smem[];
-    Sh& sh = *reinterpret_cast<Sh*>(smem);
-
+    MainShared<K>& sh = *reinterpret_cast<MainShared<K>*>(smem);
+    const Place p(a, I::CC);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int blocks = a.G * a.cpg;
-    const int item = blockIdx.x / blocks;
-    const Place p(a, item, blockIdx.x % blocks, a.cpg, CC);
-    const long long t0 = p.t0, t1 = p.t1;
-    const int sch = tid / K, m0 = (tid % K) * S, sc = p.c0 + sch;
-    const bool sc_ok = sc < p.c_end;
-    const int ech = tid % CC, etok = tid / CC, ec = p.c0 + ech;
-    const bool ec_ok = ec < p.c_end;
-    const long long slot = (long long)item * a.D + sc;
+    const int pr = tid / K, m0 = (tid % K) * S, c = p.c0 + 2 * pr;
+    const int epr = tid % I::CP, ec = p.c0 + 2 * epr;  // of the elementwise work
 
-    float A2[S] = {0.f, 0.f, 0.f, 0.f}, h[S] = {0.f, 0.f, 0.f, 0.f};
-    float carry[S] = {0.f, 0.f, 0.f, 0.f}, dA[S] = {0.f, 0.f, 0.f, 0.f};
-    if (sc_ok) {
-        load_states(A2, a.in.A + (long long)sc * a.n, m0, a.n);
-        load_states(h, a.hs + slot * a.n, m0, a.n);
-        load_states(carry, a.gs + slot * a.n, m0, a.n);
-    }
+    f2 A[2][2], h0[2][2], carry[2][2], dA[2][2];
+    load_decays(A, a, c, p.c_end, m0);
+    load_pair(h0, a.hs, a, p.item, c, p.c_end, m0);
+    load_pair(carry, a.gs, a, p.item, c, p.c_end, m0);
 #pragma unroll
-    for (int i = 0; i < S; ++i) A2[i] *= SCAN_LOG2E;
+    for (int x = 0; x < 2; ++x) dA[x][0] = dA[x][1] = pack(0.f, 0.f);
 
-    const T* up = (const T*)a.in.u + ec;
-    const T* dp = (const T*)a.in.delta + ec;
-    const T* zp = a.in.z ? (const T*)a.in.z + ec : nullptr;
-    const T* yp = (const T*)a.dy + ec;
-    const T* Bp = (const T*)a.in.B + (long long)p.g * a.n;
-    const T* Cp = (const T*)a.in.C + (long long)p.g * a.n;
-    const float dbias = a.in.delta_bias && ec_ok ? a.in.delta_bias[ec] : 0.f;
-    const float Dw = a.in.D && ec_ok ? a.in.D[ec] : 0.f;
-
-    // Forward walk: the state before each block.
-    {
-        T ru[EA], rd[EA], rB[EBA];
-        auto load = [&](long long t) {
-#pragma unroll
-            for (int e = 0; e < EA; ++e) {
-                const long long tok = t + e * K + etok;
-                const bool ok = ec_ok && tok < t1;
-                ru[e] = ok ? up[tok * a.in.ld_u] : T(0.f);
-                rd[e] = ok ? dp[tok * a.in.ld_delta] : T(0.f);
-            }
-#pragma unroll
-            for (int e = 0; e < EBA; ++e) {
-                const int idx = e * NT3 + tid, m = idx % NP;
-                const long long tok = t + idx / NP;
-                const bool ok = m < a.n && tok < t1 && idx < TA * NP;
-                rB[e] = ok ? Bp[tok * a.in.ld_b + m] : T(0.f);
-            }
-        };
-        if (t0 < t1) load(t0);
-        for (long long t = t0; t < t1; t += TA) {
-#pragma unroll
-            for (int e = 0; e < EA; ++e) {
-                float dt = to_f32(rd[e]) + dbias;
-                if (a.in.softplus) dt = softplus_f(dt);
-                if (!ec_ok || t + e * K + etok >= t1) dt = 0.f;
-                sh.u.a.dtu[e * K + etok][ech] = make_float2(dt, dt * to_f32(ru[e]));
-            }
-#pragma unroll
-            for (int e = 0; e < EBA; ++e) {
-                const int idx = e * NT3 + tid;
-                if (idx < TA * NP) (&sh.u.a.b[0][0])[idx] = to_f32(rB[e]);
-            }
-            __syncthreads();
-            if (t + TA < t1) load(t + TA);
+    I in(a, p);
+    const f2 bias = channel_pair(a.in.delta_bias, ec, p.c_end);
+    const f2 Dw = channel_pair(a.in.D, ec, p.c_end);
+    const f2 zero = pack(0.f, 0.f), one = pack(1.f, 1.f), minus = pack(-1.f, -1.f);
+    f2 dD = zero, db = zero;
+    const int len = (int)(p.t1 - p.t0), nblk = (len + BLK - 1) / BLK;
+    if (nblk > 0) in.load(nblk - 1, len - (nblk - 1) * BLK - 1);
 #pragma unroll 1
-            for (int tb = 0; tb < TA; tb += BLK) {
-                const int blk = (int)(t - t0 + tb) / BLK;
-                if (blk < LEN / BLK) sh.ck[blk][tid] = make_float4(h[0], h[1], h[2], h[3]);
+    for (int b = nblk - 1; b >= 0; --b) {
+        const int rmax = min(BLK, len - b * BLK) - 1;
+        fill_block<T, K, VEC>(sh.in, in, a.n, rmax, bias, a.in.softplus);
+        Pair<T, VEC> cu[I::E], cd[I::E], cz[I::E], cy[I::E];
 #pragma unroll
-                for (int q = 0; q < BLK; ++q) {
-                    const float2 d = sh.u.a.dtu[tb + q][sch];
-                    const float4 b4 = *reinterpret_cast<const float4*>(&sh.u.a.b[tb + q][m0]);
-                    const float bv[S] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                    for (int i = 0; i < S; ++i)
-                        h[i] = fmaf(ex2(d.x * A2[i]), h[i], d.y * bv[i]);
-                }
-            }
-            __syncthreads();
-        }
-    }
-
-    // Blocks of 8 tokens, last to first.
-    T ru[E], rd[E], rz[E], ry[E], rB[EB], rC[EB];
-    auto load = [&](long long t) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int row = e * K + etok;
-            const long long tok = t + row;
-            const bool ok = ec_ok && tok < t1 && row < BLK;
-            ru[e] = ok ? up[tok * a.in.ld_u] : T(0.f);
-            rd[e] = ok ? dp[tok * a.in.ld_delta] : T(0.f);
-            ry[e] = ok ? yp[tok * a.ld_dy] : T(0.f);
-            rz[e] = ok && zp ? zp[tok * a.in.ld_z] : T(0.f);
-        }
-#pragma unroll
-        for (int e = 0; e < EB; ++e) {
-            const int idx = e * NT3 + tid, m = idx % NP;
-            const long long tok = t + idx / NP;
-            const bool ok = m < a.n && tok < t1 && idx < BLK * NP;
-            rB[e] = ok ? Bp[tok * a.in.ld_b + m] : T(0.f);
-            rC[e] = ok ? Cp[tok * a.in.ld_c + m] : T(0.f);
-        }
-    };
-    float dD = 0.f, db = 0.f;
-    const int nblk = (int)((t1 - t0 + BLK - 1) / BLK);
-    if (nblk > 0) load(t0 + (nblk - 1) * BLK);
-    auto& B = sh.u.b;
-#pragma unroll 1
-    for (int blk = nblk - 1; blk >= 0; --blk) {
-        const long long t = t0 + blk * BLK;
-        float eu[E], ed[E], edt[E], ez[E], ey[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int row = e * K + etok;
-            eu[e] = to_f32(ru[e]);
-            ed[e] = to_f32(rd[e]) + dbias;
-            ez[e] = to_f32(rz[e]);
-            ey[e] = to_f32(ry[e]);
-            float dt = a.in.softplus ? softplus_f(ed[e]) : ed[e];
-            if (!ec_ok || t + row >= t1) dt = 0.f;
-            edt[e] = dt;
-            if (row < BLK) {
-                B.dtu[row][ech] = make_float2(dt, dt * eu[e]);
-                B.dyz[row][ech] = zp ? ey[e] * ez[e] * sigmoid_f(ez[e]) : ey[e];
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < EB; ++e) {
-            const int idx = e * NT3 + tid;
-            if (idx < BLK * NP) {
-                (&B.bc[0][0][0])[idx] = to_f32(rB[e]);
-                (&B.bc[1][0][0])[idx] = to_f32(rC[e]);
-            }
-        }
+        for (int e = 0; e < I::E; ++e) cu[e] = in.u[e], cd[e] = in.d[e], cz[e] = in.z[e], cy[e] = in.y[e];
         __syncthreads();
-        if (blk > 0) load(t - BLK);
+        if (b > 0) in.load(b - 1, BLK - 1);
 
-        float hb[BLK][S], av[BLK][S];  // the state before each token, and its decay
-        {
-            const float4 c = sh.ck[blk][tid];
-            h[0] = c.x, h[1] = c.y, h[2] = c.z, h[3] = c.w;
+        // The state before the block: its local part, and what is left of the
+        // state before the chunk.
+        f2 hb[BLK + 1][2][2];
+        if (b == 0) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) hb[0][x][0] = h0[x][0], hb[0][x][1] = h0[x][1];
+        } else {
+            const long long at = (long long)p.item * (LEN / BLK) + b;
+            load_pair(hb[0], a.ck, a, at, c, p.c_end, m0);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float d = c + x < p.c_end ? a.ckdt[at * a.D + c + x] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    hb[0][x][i] = fma2(ex2_2(mul2(pack(d, d), A[x][i])), h0[x][i], hb[0][x][i]);
+            }
         }
 #pragma unroll
         for (int q = 0; q < BLK; ++q) {
-            const float2 d = B.dtu[q][sch];
-            const float4 b4 = *reinterpret_cast<const float4*>(&B.bc[0][q][m0]);
-            const float bv[S] = {b4.x, b4.y, b4.z, b4.w};
+            const float4 d = sh.in.dt[q][pr];
+            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.in.b[q][m0]);
+            const float dt[2] = {d.x, d.z}, du[2] = {d.y, d.w};
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                hb[q][i] = h[i];
-                av[q][i] = ex2(d.x * A2[i]);
-                h[i] = fmaf(av[q][i], h[i], d.y * bv[i]);
-            }
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    hb[q + 1][x][i] = fma2(ex2_2(mul2(pack(dt[x], dt[x]), A[x][i])), hb[q][x][i],
+                                           mul2(pack(du[x], du[x]), i ? bv.y : bv.x));
         }
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-            float gB[4], gA[4], yv[4];
+        for (int q = BLK - 1; q >= 0; --q) {
+            const float4 d = sh.in.dt[q][pr];
+            float w[2];
+            unpack(sh.in.w[q][pr], w[0], w[1]);
+            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.in.b[q][m0]);
+            const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&sh.in.c[q][m0]);
+            const float dt[2] = {d.x, d.z}, du[2] = {d.y, d.w};
+            f2 dB[2], dC[2];
+            float gB[2], gA[2], y[2];
 #pragma unroll
-            for (int r = 3; r >= 0; --r) {
-                const int q = half * 4 + r;
-                const float2 d = B.dtu[q][sch];
-                const float w = B.dyz[q][sch];
-                const float4 b4 = *reinterpret_cast<const float4*>(&B.bc[0][q][m0]);
-                const float4 c4 = *reinterpret_cast<const float4*>(&B.bc[1][q][m0]);
-                const float bv[S] = {b4.x, b4.y, b4.z, b4.w}, cv[S] = {c4.x, c4.y, c4.z, c4.w};
-                float v[8];
-                gB[r] = gA[r] = yv[r] = 0.f;
+            for (int x = 0; x < 2; ++x) {
+                const f2 ww = pack(w[x], w[x]), dd = pack(dt[x], dt[x]), uu = pack(du[x], du[x]);
+                f2 sB, sA, sy;
 #pragma unroll
-                for (int i = 0; i < S; ++i) {
-                    const float ht = q == BLK - 1 ? h[i] : hb[q < BLK - 1 ? q + 1 : q][i];
-                    const float g = fmaf(cv[i], w, carry[i]);
-                    v[i] = g * d.y;
-                    v[S + i] = w * ht;
-                    yv[r] = fmaf(cv[i], ht, yv[r]);
-                    gB[r] = fmaf(g, bv[i], gB[r]);
-                    carry[i] = av[q][i] * g;
-                    const float gh = carry[i] * hb[q][i];
-                    gA[r] = fmaf(A2[i], gh, gA[r]);
-                    dA[i] = fmaf(gh, d.x, dA[i]);
+                for (int i = 0; i < 2; ++i) {
+                    const f2 Bm = i ? bv.y : bv.x, Cm = i ? cv.y : cv.x, ht = hb[q + 1][x][i];
+                    const f2 g = fma2(Cm, ww, carry[x][i]);
+                    dB[i] = x ? fma2(g, uu, dB[i]) : mul2(g, uu);
+                    dC[i] = x ? fma2(ht, ww, dC[i]) : mul2(ht, ww);
+                    sB = i ? fma2(g, Bm, sB) : mul2(g, Bm);
+                    sy = i ? fma2(ht, Cm, sy) : mul2(ht, Cm);
+                    float A0, A1;
+                    unpack(A[x][i], A0, A1);
+                    carry[x][i] = mul2(pack(ex2_again(dt[x] * A0), ex2_again(dt[x] * A1)), g);
+                    const f2 gh = mul2(carry[x][i], hb[q][x][i]);
+                    sA = i ? fma2(gh, A[x][i], sA) : mul2(gh, A[x][i]);
+                    dA[x][i] = fma2(gh, dd, dA[x][i]);
                 }
-                lane_reduce<8, M, K>(v, lane);
-                if (reduced_writer<8, M, K>(lane)) {
-                    const int at = reduced_index<8, M, K>(lane);
-#pragma unroll
-                    for (int x = 0; x < RC; ++x) {
-                        const int idx = at + x;
-                        B.red[idx / S][warp][q][m0 + idx % S] = v[x];
-                    }
-                }
+                float lo, hi;
+                unpack(sB, lo, hi);
+                gB[x] = lo + hi;
+                unpack(sA, lo, hi);
+                gA[x] = lo + hi;
+                unpack(sy, lo, hi);
+                y[x] = lo + hi;
             }
-            lane_reduce<4, K, 1>(gB, lane);
-            lane_reduce<4, K, 1>(gA, lane);
-            lane_reduce<4, K, 1>(yv, lane);
-            if (reduced_writer<4, K, 1>(lane)) {
-                const int at = half * 4 + reduced_index<4, K, 1>(lane);
+            sh.gB[q][tid] = pack(gB[0], gB[1]);
+            sh.gA[q][tid] = pack(gA[0], gA[1]);
+            sh.y[q][tid] = pack(y[0], y[1]);
+            float v[8];
+            unpack(dB[0], v[0], v[1]);
+            unpack(dB[1], v[2], v[3]);
+            unpack(dC[0], v[4], v[5]);
+            unpack(dC[1], v[6], v[7]);
+            lane_reduce<8, M, K>(v, lane);
+            if (reduced_writer<8, M, K>(lane)) {
+                const int at = reduced_index<8, M, K>(lane);
 #pragma unroll
-                for (int r = 0; r < RK; ++r) {
-                    B.gB[at + r][sch] = gB[r];
-                    B.gA[at + r][sch] = gA[r];
-                    B.y[at + r][sch] = yv[r];
-                }
+                for (int i = 0; i < RC; ++i) sh.red[warp][q][(at + i) / S][m0 + (at + i) % S] = v[i];
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int row = e * K + etok;
-            const long long tok = t + row;
-            if (ec_ok && tok < t1 && row < BLK) {
-                const float u = eu[e], gb = B.gB[row][ech];
-                float w = ey[e];
-                if (zp) {
-                    const float sg = sigmoid_f(ez[e]), gate = ez[e] * sg;
-                    const float y = fmaf(Dw, u, B.y[row][ech]);
-                    store_out<T>(a.out.dz, tok * a.D + ec, w * y * (sg + gate * (1.f - sg)),
-                                 a.out_f32);
-                    w *= gate;
-                }
-                store_out<T>(a.out.du, tok * a.D + ec, fmaf(Dw, w, edt[e] * gb), a.out_f32);
-                float dd = fmaf(SCAN_LN2, B.gA[row][ech], u * gb);
-                if (a.in.softplus) dd *= sigmoid_f(ed[e]);
-                store_out<T>(a.out.ddelta, tok * a.D + ec, dd, a.out_f32);
-                dD = fmaf(w, u, dD);
-                db += dd;
+        for (int e = 0; e < I::E; ++e) {
+            const int row = in.prow + e * I::RP;
+            if (row > rmax || !in.lo_ok) continue;
+            const long long tok = p.t0 + b * BLK + row;
+            const f2 u = cu[e].get(), gb = sum_shares<K>(&sh.gB[row][epr * K]);
+            const f2 ga = sum_shares<K>(&sh.gA[row][epr * K]);
+            f2 w = cy[e].get();
+            if (in.gated) {
+                const f2 z = cz[e].get(), sg = sigmoid2(z), gate = mul2(z, sg);
+                const f2 y = fma2(Dw, u, sum_shares<K>(&sh.y[row][epr * K]));
+                // (z sg)' = sg + z sg (1 - sg)
+                const f2 slope = fma2(gate, fma2(sg, minus, one), sg);
+                store_two<T, K, VEC>(a, a.out.dz, tok, ec, in.hi_ok, mul2(mul2(w, y), slope));
+                w = mul2(w, gate);
             }
+            const float4 dtv = sh.in.dt[row][epr];
+            const f2 dt = pack(dtv.x, dtv.z);
+            store_two<T, K, VEC>(a, a.out.du, tok, ec, in.hi_ok, fma2(Dw, w, mul2(dt, gb)));
+            f2 dd = fma2(ga, pack(SCAN_LN2, SCAN_LN2), mul2(u, gb));
+            if (a.in.softplus) dd = mul2(dd, softplus_slope2(add2(cd[e].get(), bias)));
+            store_two<T, K, VEC>(a, a.out.ddelta, tok, ec, in.hi_ok, dd);
+            dD = fma2(w, u, dD);
+            db = add2(db, dd);
         }
-        for (int idx = tid; idx < 2 * BLK * NP; idx += NT3) {
-            const int m = idx % NP, q = idx / NP % BLK, which = idx / (NP * BLK);
+        for (int i = tid; i < 2 * BLK * NP; i += NT) {
+            const int m = i % NP, which = i / NP % 2, q = i / (2 * NP);
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < NT3 / 32; ++w) v += B.red[which][w][q][m];
-            if (m < a.n && t + q < t1) {
+            for (int k = 0; k < NT / 32; ++k) v += sh.red[k][q][which][m];
+            if (m < a.n && q <= rmax) {
                 float* to = which ? a.dCp : a.dBp;
-                to[(((long long)p.cbg * a.view.total + t + q) * a.G + p.g) * a.n + m] = v;
+                const long long tok = p.t0 + b * BLK + q;
+                to[(((long long)p.cbg * a.view.total + tok) * a.G + p.g) * a.n + m] = v;
             }
         }
+        __syncthreads();
     }
-    if (sc_ok) store_states(a.hs + slot * a.n, dA, m0, a.n);  // this thread's own, read above
-    // dD and ddelta_bias of this chunk: K threads hold one channel's.
+    store_pair(a.hs, dA, a, p.item, c, p.c_end, m0);  // this thread's own slots, read above
+    // dD and ddelta_bias of this chunk: RP threads hold one pair of channels.
+    ulonglong2* pair = reinterpret_cast<ulonglong2*>(&sh.gB[0][0]);
+    pair[tid] = make_ulonglong2(dD, db);
     __syncthreads();
-    float* red = &B.red[0][0][0][0];
-    float2* pair = reinterpret_cast<float2*>(red);
-    pair[tid] = make_float2(dD, db);
-    __syncthreads();
-    if (tid < CC && ec_ok) {
-        float x = 0.f, y = 0.f;
+    if (tid < I::CP && in.lo_ok) {
+        f2 x = zero, y = zero;
 #pragma unroll
-        for (int k = 0; k < K; ++k) x += pair[tid + k * CC].x, y += pair[tid + k * CC].y;
-        a.dDp[(long long)item * a.D + ec] = x;
-        a.dbp[(long long)item * a.D + ec] = y;
+        for (int k = 0; k < I::RP; ++k) {
+            x = add2(x, pair[tid + k * I::CP].x);
+            y = add2(y, pair[tid + k * I::CP].y);
+        }
+        float x0, x1, y0, y1;
+        unpack(x, x0, x1);
+        unpack(y, y0, y1);
+        const long long at = (long long)p.item * a.D + ec;
+        a.dDp[at] = x0;
+        a.dbp[at] = y0;
+        if (in.hi_ok) a.dDp[at + 1] = x1, a.dbp[at + 1] = y1;
     }
 }
 
@@ -507,7 +569,9 @@ __global__ void __launch_bounds__(256) sum_bc_kernel(BackArgs a)
     float v = 0.f;
 #pragma unroll 8
     for (int r = 0; r < a.cpg; ++r) v += in[r * slab];
-    store_out<float>(blockIdx.y ? a.out.dC : a.out.dB, i, v, a.out_f32);
+    void* out = blockIdx.y ? a.out.dC : a.out.dB;
+    if (a.out_f32) ((float*)out)[i] = v;
+    else ((__nv_bfloat16*)out)[i] = __float2bfloat16_rn(v);
 }
 
 // out[c] = sum of in[r][c]: 32 columns per CTA, 32 strands of rows.
@@ -531,15 +595,21 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* in, float
     if (x == 0 && oc < cols) out[oc] = v;
 }
 
+// Lanes per pair of channels.
+int back_lanes(int n)
+{
+    return n <= 8 ? 2 : scan_lanes(n);
+}
+
 struct BackLayout {
     int items, cpg;
-    size_t hs, gs, dtsum, dDp, dbp, dBp, dCp, first, bytes;
+    size_t hs, gs, dtsum, ck, ckdt, dDp, dbp, dBp, dCp, first, bytes;
 };
 
 BackLayout back_layout(int G, int D, long long total, int n, int num_seqs)
 {
     BackLayout l;
-    const int CC = NT3 / scan_lanes(n);
+    const int CC = 2 * NT / back_lanes(n);
     l.items = (int)(total / LEN + num_seqs);
     l.cpg = (D / G + CC - 1) / CC;
     size_t at = 0;
@@ -552,6 +622,8 @@ BackLayout back_layout(int G, int D, long long total, int n, int num_seqs)
     l.hs = take(states);
     l.gs = take(states);
     l.dtsum = take(chans);
+    l.ck = take(states * (LEN / BLK));
+    l.ckdt = take(chans * (LEN / BLK));
     l.dDp = take(chans);
     l.dbp = take(chans);
     const size_t slabs = (size_t)l.cpg * total * G * n * 4;
@@ -582,7 +654,7 @@ cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, co
                                  long long ld_dy, const float* dstate_out,
                                  const la_scan_grads& out, void* ws, cudaStream_t stream)
 {
-    const int K = scan_lanes(p.n), num_seqs = p.view.num_seqs, Dg = p.D / p.G;
+    const int num_seqs = p.view.num_seqs;
     const BackLayout l = back_layout(p.G, p.D, p.view.total, p.n, num_seqs);
     char* w = (char*)ws;
     BackArgs a{};
@@ -594,6 +666,8 @@ cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, co
     a.hs = (float*)(w + l.hs);
     a.gs = (float*)(w + l.gs);
     a.dtsum = (float*)(w + l.dtsum);
+    a.ck = (float*)(w + l.ck);
+    a.ckdt = (float*)(w + l.ckdt);
     a.dDp = (float*)(w + l.dDp);
     a.dbp = (float*)(w + l.dbp);
     a.dBp = (float*)(w + l.dBp);
@@ -622,24 +696,37 @@ cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, co
     cudaError_t e = cudaSuccess;
     const long long DN = (long long)p.D * p.n;
     if (num_seqs > 0) {
-        const int CC1 = NT1 / K, cpg1 = (Dg + CC1 - 1) / CC1;
-        const unsigned grid1 = (unsigned)((long long)a.ch.items * p.G * cpg1);
-        const unsigned grid3 = (unsigned)((long long)a.ch.items * p.G * a.cpg);
-        const unsigned grid2 = (unsigned)((DN + 127) / 128 * num_seqs);
-#define LA_CALL(KK)                                                                              \
+        const unsigned grid = (unsigned)((long long)a.ch.items * p.G * a.cpg);
+        const unsigned combine_grid = (unsigned)((DN + 127) / 128 * num_seqs);
+        const size_t two = p.in_t == LA_BF16 ? 4 : 8;  // bytes of a pair of channels
+        const auto pairs = [&](const void* q, long long ld) {
+            return (uintptr_t)q % two == 0 && ld % 2 == 0;
+        };
+        const bool vec = p.D / p.G % 2 == 0 && pairs(p.in.u, p.in.ld_u) &&
+                         pairs(p.in.delta, p.in.ld_delta) && pairs(dy, ld_dy) &&
+                         (!p.in.z || pairs(p.in.z, p.in.ld_z));
+#define LA_TYPE(T, KK)                                                                           \
     do {                                                                                         \
+        auto local = vec ? local_kernel<T, KK, true> : local_kernel<T, KK, false>;               \
+        auto main = vec ? main_kernel<T, KK, true> : main_kernel<T, KK, false>;                  \
         const int smem = (int)sizeof(MainShared<KK>);                                            \
-        auto main = p.in_t == LA_BF16 ? main_kernel<__nv_bfloat16, KK> : main_kernel<float, KK>; \
-        auto local =                                                                             \
-            p.in_t == LA_BF16 ? local_kernel<__nv_bfloat16, KK> : local_kernel<float, KK>;       \
         e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);       \
         if (e != cudaSuccess) return e;                                                          \
-        local<<<grid1, NT1, 0, stream>>>(a, cpg1);                                               \
-        combine_kernel<<<grid2, 128, 0, stream>>>(a, state_in, dstate_out);                      \
-        main<<<grid3, NT3, smem, stream>>>(a);                                                   \
+        local<<<grid, NT, 0, stream>>>(a);                                                       \
+        combine_kernel<<<combine_grid, 128, 0, stream>>>(a, state_in, dstate_out);               \
+        main<<<grid, NT, smem, stream>>>(a);                                                     \
     } while (0)
-        LA_SCAN_DISPATCH_K(p.n, LA_CALL)
+#define LA_CALL(KK)                                                                              \
+    if (p.in_t == LA_BF16) LA_TYPE(__nv_bfloat16, KK);                                           \
+    else LA_TYPE(float, KK)
+        switch (back_lanes(p.n)) {
+        case 2: LA_CALL(2); break;
+        case 4: LA_CALL(4); break;
+        case 8: LA_CALL(8); break;
+        default: LA_CALL(16); break;
+        }
 #undef LA_CALL
+#undef LA_TYPE
         count_launch(3);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if (p.view.total > 0) {
