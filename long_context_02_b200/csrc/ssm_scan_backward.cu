@@ -1,6 +1,6 @@
 // Gradients of the selective scan (formulas in lightning.h).
 //
-// The sequences are cut into chunks of LEN tokens, all of them independent:
+// The sequences are cut into chunks of 32 to 128 tokens, all of them independent:
 //  1. local pass: each chunk's state from zero, h_c, and that state before every
 //     block of 8 tokens; the sums of dt to the same places, whose exponentials
 //     exp(A sum dt) are the decays from the chunk's start; and the gradient that
@@ -26,7 +26,6 @@
 namespace la {
 namespace {
 
-constexpr int LEN = 128;  // tokens per chunk
 constexpr int BLK = 8;    // tokens per block
 constexpr int NT = 128;   // threads per CTA of the local and the main pass
 
@@ -40,8 +39,8 @@ struct BackArgs {
     float* hs;      // [items][D][n]: chunk states, then states before the chunks, then dA partials
     float* gs;      // [items][D][n]: G of the chunks, then gradients of the states after them
     float* dtsum;   // [items][D]
-    float* ck;      // [items][LEN / BLK][D][n]: local state before each block but the first
-    float* ckdt;    // [items][LEN / BLK][D]: sum of the chunk's dt before each block
+    float* ck;      // [items][len / BLK][D][n]: local state before each block but the first
+    float* ckdt;    // [items][len / BLK][D]: sum of the chunk's dt before each block
     float* dDp;     // [items][D]
     float* dbp;     // [items][D]
     float* dBp;     // [cpg][total][G][n]
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(NT, 4) local_kernel(BackArgs a)
         __syncthreads();
         if (b + 1 < nblk) in.load(b + 1, min(BLK, len - (b + 1) * BLK) - 1);
         if (b > 0) {
-            const long long at = (long long)p.item * (LEN / BLK) + b;
+            const long long at = (long long)p.item * (a.ch.len / BLK) + b;
             store_pair(a.ck, h, a, at, c, p.c_end, m0);
             if (m0 == 0) {
                 float d0, d1;
@@ -307,19 +306,36 @@ __global__ void __launch_bounds__(128) combine_kernel(BackArgs a, const float* s
     const int first = a.ch.first_of(s), end = a.ch.end_of(s);
     float h = state_in ? state_in[s * DN + e] : 0.f;
     float g = dstate_out ? dstate_out[s * DN + e] : 0.f;
-#pragma unroll 4
-    for (int i = first; i < end; ++i) {
-        const float local = a.hs[i * DN + e];
-        const float decay = ex2(A2 * a.dtsum[(long long)i * a.D + c]);
-        a.hs[i * DN + e] = h;
-        h = fmaf(decay, h, local);
+    // Reads of AHEAD chunks at a time, before the writes to the same places.
+    constexpr int AHEAD = 8;
+    float local[AHEAD], decay[AHEAD];
+    for (int i = first; i < end; i += AHEAD) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const long long at = i + k < end ? i + k : end - 1;
+            local[k] = a.hs[at * DN + e];
+            decay[k] = a.dtsum[at * a.D + c];
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i + k < end) {
+                a.hs[(i + k) * DN + e] = h;
+                h = fmaf(ex2(A2 * decay[k]), h, local[k]);
+            }
     }
-#pragma unroll 4
-    for (int i = end - 1; i >= first; --i) {
-        const float local = a.gs[i * DN + e];
-        const float decay = ex2(A2 * a.dtsum[(long long)i * a.D + c]);
-        a.gs[i * DN + e] = g;
-        g = fmaf(decay, g, local);
+    for (int i = end - 1; i >= first; i -= AHEAD) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const long long at = i - k >= first ? i - k : first;
+            local[k] = a.gs[at * DN + e];
+            decay[k] = a.dtsum[at * a.D + c];
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (i - k >= first) {
+                a.gs[(i - k) * DN + e] = g;
+                g = fmaf(ex2(A2 * decay[k]), g, local[k]);
+            }
     }
     if (a.out.dstate_in) a.out.dstate_in[s * DN + e] = g;
 }
@@ -417,83 +433,114 @@ __global__ void __launch_bounds__(NT, 3) main_kernel(BackArgs a)
 
         // The state before the block: its local part, and what is left of the
         // state before the chunk.
-        f2 hb[BLK + 1][2][2];
+        f2 start[2][2];
         if (b == 0) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) hb[0][x][0] = h0[x][0], hb[0][x][1] = h0[x][1];
+            for (int x = 0; x < 2; ++x) start[x][0] = h0[x][0], start[x][1] = h0[x][1];
         } else {
-            const long long at = (long long)p.item * (LEN / BLK) + b;
-            load_pair(hb[0], a.ck, a, at, c, p.c_end, m0);
+            const long long at = (long long)p.item * (a.ch.len / BLK) + b;
+            load_pair(start, a.ck, a, at, c, p.c_end, m0);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float d = c + x < p.c_end ? a.ckdt[at * a.D + c + x] : 0.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    hb[0][x][i] = fma2(ex2_2(mul2(pack(d, d), A[x][i])), h0[x][i], hb[0][x][i]);
+                    start[x][i] = fma2(ex2_2(mul2(pack(d, d), A[x][i])), h0[x][i], start[x][i]);
             }
         }
-#pragma unroll
-        for (int q = 0; q < BLK; ++q) {
+        auto advance = [&](int q, const f2 (*from)[2], f2 (*to)[2]) {
             const float4 d = sh.in.dt[q][pr];
             const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.in.b[q][m0]);
             const float dt[2] = {d.x, d.z}, du[2] = {d.y, d.w};
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    hb[q + 1][x][i] = fma2(ex2_2(mul2(pack(dt[x], dt[x]), A[x][i])), hb[q][x][i],
-                                           mul2(pack(du[x], du[x]), i ? bv.y : bv.x));
-        }
-#pragma unroll
-        for (int q = BLK - 1; q >= 0; --q) {
-            const float4 d = sh.in.dt[q][pr];
-            float w[2];
-            unpack(sh.in.w[q][pr], w[0], w[1]);
-            const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.in.b[q][m0]);
-            const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&sh.in.c[q][m0]);
-            const float dt[2] = {d.x, d.z}, du[2] = {d.y, d.w};
-            f2 dB[2], dC[2];
-            float gB[2], gA[2], y[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const f2 ww = pack(w[x], w[x]), dd = pack(dt[x], dt[x]), uu = pack(du[x], du[x]);
-                f2 sB, sA, sy;
-#pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const f2 Bm = i ? bv.y : bv.x, Cm = i ? cv.y : cv.x, ht = hb[q + 1][x][i];
-                    const f2 g = fma2(Cm, ww, carry[x][i]);
-                    dB[i] = x ? fma2(g, uu, dB[i]) : mul2(g, uu);
-                    dC[i] = x ? fma2(ht, ww, dC[i]) : mul2(ht, ww);
-                    sB = i ? fma2(g, Bm, sB) : mul2(g, Bm);
-                    sy = i ? fma2(ht, Cm, sy) : mul2(ht, Cm);
                     float A0, A1;
                     unpack(A[x][i], A0, A1);
-                    carry[x][i] = mul2(pack(ex2_again(dt[x] * A0), ex2_again(dt[x] * A1)), g);
-                    const f2 gh = mul2(carry[x][i], hb[q][x][i]);
-                    sA = i ? fma2(gh, A[x][i], sA) : mul2(gh, A[x][i]);
-                    dA[x][i] = fma2(gh, dd, dA[x][i]);
+                    to[x][i] = fma2(pack(ex2_again(dt[x] * A0), ex2_again(dt[x] * A1)), from[x][i],
+                                    mul2(pack(du[x], du[x]), i ? bv.y : bv.x));
                 }
-                float lo, hi;
-                unpack(sB, lo, hi);
-                gB[x] = lo + hi;
-                unpack(sA, lo, hi);
-                gA[x] = lo + hi;
-                unpack(sy, lo, hi);
-                y[x] = lo + hi;
-            }
-            sh.gB[q][tid] = pack(gB[0], gB[1]);
-            sh.gA[q][tid] = pack(gA[0], gA[1]);
-            sh.y[q][tid] = pack(y[0], y[1]);
+        };
+        // What a token leaves is written while the next one is worked on, and after
+        // that one's inputs are read: shared reads stay behind earlier writes, and
+        // these wait for the shuffles.
+        struct {
             float v[8];
-            unpack(dB[0], v[0], v[1]);
-            unpack(dB[1], v[2], v[3]);
-            unpack(dC[0], v[4], v[5]);
-            unpack(dC[1], v[6], v[7]);
-            lane_reduce<8, M, K>(v, lane);
+            f2 gB, gA, y;
+        } last;
+        auto flush = [&](int q) {
+            sh.gB[q][tid] = last.gB;
+            sh.gA[q][tid] = last.gA;
+            sh.y[q][tid] = last.y;
+            lane_reduce<8, M, K>(last.v, lane);
             if (reduced_writer<8, M, K>(lane)) {
                 const int at = reduced_index<8, M, K>(lane);
 #pragma unroll
-                for (int i = 0; i < RC; ++i) sh.red[warp][q][(at + i) / S][m0 + (at + i) % S] = v[i];
+                for (int i = 0; i < RC; ++i)
+                    sh.red[warp][q][(at + i) / S][m0 + (at + i) % S] = last.v[i];
+            }
+        };
+        // Half a block at a time: its states stay in registers.
+        constexpr int HALF = BLK / 2;
+#pragma unroll 1
+        for (int from = HALF; from >= 0; from -= HALF) {
+            f2 hb[HALF + 1][2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) hb[0][x][0] = start[x][0], hb[0][x][1] = start[x][1];
+            if (from) {
+#pragma unroll
+                for (int q = 0; q < HALF; ++q) advance(q, hb[0], hb[0]);
+            }
+#pragma unroll
+            for (int r = 0; r < HALF; ++r) advance(from + r, hb[r], hb[r + 1]);
+#pragma unroll
+            for (int r = HALF - 1; r >= 0; --r) {
+                const int q = from + r;
+                const float4 d = sh.in.dt[q][pr];
+                float w[2];
+                unpack(sh.in.w[q][pr], w[0], w[1]);
+                const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(&sh.in.b[q][m0]);
+                const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(&sh.in.c[q][m0]);
+                if (r < HALF - 1) flush(q + 1);
+                const float dt[2] = {d.x, d.z}, du[2] = {d.y, d.w};
+                f2 dB[2], dC[2];
+                float gB[2], gA[2], y[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const f2 ww = pack(w[x], w[x]), dd = pack(dt[x], dt[x]), uu = pack(du[x], du[x]);
+                    f2 sB, sA, sy;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const f2 Bm = i ? bv.y : bv.x, Cm = i ? cv.y : cv.x, ht = hb[r + 1][x][i];
+                        const f2 g = fma2(Cm, ww, carry[x][i]);
+                        dB[i] = x ? fma2(g, uu, dB[i]) : mul2(g, uu);
+                        dC[i] = x ? fma2(ht, ww, dC[i]) : mul2(ht, ww);
+                        sB = i ? fma2(g, Bm, sB) : mul2(g, Bm);
+                        sy = i ? fma2(ht, Cm, sy) : mul2(ht, Cm);
+                        float A0, A1;
+                        unpack(A[x][i], A0, A1);
+                        carry[x][i] = mul2(pack(ex2_again(dt[x] * A0), ex2_again(dt[x] * A1)), g);
+                        const f2 gh = mul2(carry[x][i], hb[r][x][i]);
+                        sA = i ? fma2(gh, A[x][i], sA) : mul2(gh, A[x][i]);
+                        dA[x][i] = fma2(gh, dd, dA[x][i]);
+                    }
+                    float lo, hi;
+                    unpack(sB, lo, hi);
+                    gB[x] = lo + hi;
+                    unpack(sA, lo, hi);
+                    gA[x] = lo + hi;
+                    unpack(sy, lo, hi);
+                    y[x] = lo + hi;
+                }
+                last.gB = pack(gB[0], gB[1]);
+                last.gA = pack(gA[0], gA[1]);
+                last.y = pack(y[0], y[1]);
+                unpack(dB[0], last.v[0], last.v[1]);
+                unpack(dB[1], last.v[2], last.v[3]);
+                unpack(dC[0], last.v[4], last.v[5]);
+                unpack(dC[1], last.v[6], last.v[7]);
+                if (r == 0) flush(q);
             }
         }
         __syncthreads();
@@ -602,7 +649,7 @@ int back_lanes(int n)
 }
 
 struct BackLayout {
-    int items, cpg;
+    int len, items, cpg;
     size_t hs, gs, dtsum, ck, ckdt, dDp, dbp, dBp, dCp, first, bytes;
 };
 
@@ -610,8 +657,12 @@ BackLayout back_layout(int G, int D, long long total, int n, int num_seqs)
 {
     BackLayout l;
     const int CC = 2 * NT / back_lanes(n);
-    l.items = (int)(total / LEN + num_seqs);
     l.cpg = (D / G + CC - 1) / CC;
+    // Tokens per chunk: 128, or fewer while that leaves SMs without work (three
+    // CTAs fit on each): a chunk is walked by one CTA from end to end.
+    l.len = 128;
+    while (l.len > 32 && (total / l.len + 1) * G * l.cpg < 3 * 148) l.len /= 2;
+    l.items = (int)(total / l.len + num_seqs);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -622,8 +673,8 @@ BackLayout back_layout(int G, int D, long long total, int n, int num_seqs)
     l.hs = take(states);
     l.gs = take(states);
     l.dtsum = take(chans);
-    l.ck = take(states * (LEN / BLK));
-    l.ckdt = take(chans * (LEN / BLK));
+    l.ck = take(states * (l.len / BLK));
+    l.ckdt = take(chans * (l.len / BLK));
     l.dDp = take(chans);
     l.dbp = take(chans);
     const size_t slabs = (size_t)l.cpg * total * G * n * 4;
@@ -677,19 +728,19 @@ cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, co
     a.n = p.n;
     a.cpg = l.cpg;
     a.out_f32 = p.out_t == LA_F32;
-    a.ch.len = LEN;
+    a.ch.len = l.len;
     if (p.view.cu) {
         int* first = (int*)(w + l.first);
         a.ch.items = l.items;
         a.ch.first = first;
         a.ch.seq_of = first + num_seqs + 1;
         if (num_seqs > 0) {
-            cudaError_t e = launch_plan_chunks(p.view, LEN, l.items, first, first + num_seqs + 1,
+            cudaError_t e = launch_plan_chunks(p.view, l.len, l.items, first, first + num_seqs + 1,
                                                stream);
             if (e != cudaSuccess) return e;
         }
     } else if (num_seqs > 0) {
-        const long long per = (p.view.N + LEN - 1) / LEN;
+        const long long per = (p.view.N + l.len - 1) / l.len;
         a.ch.per_seq = per > 1 ? (int)per : 1;
         a.ch.items = a.ch.per_seq * num_seqs;
     }
