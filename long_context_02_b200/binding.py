@@ -10,6 +10,7 @@ other implementation to fall back to. If the library has not been built,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -321,24 +322,24 @@ def backward(dout, q, k, v, slopes, out_dtype=None, stream=None):
 
 def _rows(t, lead, inner, what):
     """Pointer of a token tensor [*lead, *inner] and the elements between its tokens."""
-    k = len(lead)
-    shape, stride = t.shape, t.stride()
-    if shape[:k] != lead or shape[k:] != inner:
-        raise ValueError(f"{what} is {tuple(shape)}, expected {tuple(lead) + tuple(inner)}")
-    dense = 1
+    if t.shape != lead + inner:
+        raise ValueError(f"{what} is {tuple(t.shape)}, expected {tuple(lead + inner)}")
+    dense = inner[0] if len(inner) == 1 else inner[0] * inner[1]
+    if t.is_contiguous():
+        return t.data_ptr() or None, dense
+    k, stride = len(lead), t.stride()
+    size = 1
     for n, st in zip(reversed(inner), reversed(stride[k:])):
-        if n != 1 and st != dense:
+        if n != 1 and st != size:
             raise ValueError(f"{what}: the elements of a token must be contiguous")
-        dense *= n
-    if k == 1:
-        ld = stride[0] if lead[0] > 1 else dense
-    elif lead[1] > 1:
+        size *= n
+    if k == 2 and lead[1] > 1:
         ld = stride[1]
         if lead[0] > 1 and stride[0] != lead[1] * ld:
             raise ValueError(f"{what}: the tokens of all sequences must be evenly spaced")
     else:
         ld = stride[0] if lead[0] > 1 else dense
-    return (t.data_ptr() if t.numel() else None), ld
+    return t.data_ptr() or None, ld
 
 
 def _flat(t, shape, dtype, what):
@@ -353,14 +354,14 @@ def _flat(t, shape, dtype, what):
 
 
 def _same(first, *others):
-    """Every given tensor is on first's device, which is a GPU."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, not on {dev}")
+    """Every given tensor is on first's device, which is a GPU; its index."""
+    if not first.is_cuda:
+        raise ValueError(f"tensors must be on a GPU, not on {first.device}")
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and on {t.device}")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {first.device} and on {t.device}")
+    return index
 
 
 def _sequences(x, cu_seqlens, features):
@@ -379,35 +380,25 @@ def _sequences(x, cu_seqlens, features):
                                                         "cu_seqlens")
 
 
-class _on:
-    """Makes `stream` (default: the device's current one) current for the allocations of a
-    call and for its launch, on the tensors' device. Inputs that a caller frees while the
-    call runs on another stream than theirs stay allocated until it is done."""
+_HERE_AND_NOW = contextlib.nullcontext()
 
-    def __init__(self, dev, stream, inputs):
-        self.guard = None
-        if stream is None:
-            if torch.cuda.current_device() != dev.index:
-                self.guard = torch.cuda.device(dev)
-            stream = torch.cuda.current_stream(dev)
-        else:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            if stream != torch.cuda.current_stream(dev):
-                for t in inputs:
-                    if t is not None:
-                        t.record_stream(stream)
-            self.guard = torch.cuda.stream(stream)  # makes its device current too
-        self.handle = stream.cuda_stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(index, stream, inputs):
+    """(context, raw stream) of a call on GPU `index`: within the context the
+    device is current and allocations belong to the stream (default: the
+    device's current one). Inputs that a caller frees while the call runs on
+    another stream than theirs stay allocated until it is done."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        return (_HERE_AND_NOW if torch.cuda.current_device() == index
+                else torch.cuda.device(index)), raw
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    if stream != torch.cuda.current_stream(index):
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+    return torch.cuda.stream(stream), stream.cuda_stream  # makes its device current too
 
 
 def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead):
@@ -440,7 +431,8 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     dev = _same(u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens)
     s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead)
     sp = _flat(state_in, (seqs, width, n), torch.float32, "state_in")
-    with _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens)) as handle:
+    ctx, handle = _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens))
+    with ctx:
         y = torch.empty((*lead, width), dtype=out_dtype or u.dtype, device=dev)
         state = (torch.empty((seqs, width, n), dtype=torch.float32, device=dev)
                  if want_state else None)
@@ -462,7 +454,8 @@ def selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=Non
     s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, u.shape[:1])
     seqs = u.shape[0]
     sp = _flat(state, (seqs, width, n), torch.float32, "state")
-    with _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state)) as handle:
+    ctx, handle = _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state))
+    with ctx:
         y = torch.empty((seqs, width), dtype=out_dtype or u.dtype, device=dev)
         _check("la_selective_scan_step", lib().la_selective_scan_step(
             s, sp, y.data_ptr() or None, seqs, width, G, n, _dt(u), _dt(y), handle))
@@ -484,8 +477,9 @@ def selective_scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=No
     f32 = torch.float32
     sp = _flat(state_in, (seqs, width, n), f32, "state_in")
     dsp = _flat(dstate_out, (seqs, width, n), f32, "dstate_out")
-    with _on(dev, stream, (dy, u, delta, A, B, C, D, z, delta_bias, state_in, dstate_out,
-                           cu_seqlens)) as handle:
+    ctx, handle = _on(dev, stream, (dy, u, delta, A, B, C, D, z, delta_bias, state_in, dstate_out,
+                           cu_seqlens))
+    with ctx:
         def new(shape, dtype=f32):
             return torch.empty(shape, dtype=dtype, device=dev)
 
@@ -529,7 +523,8 @@ def short_conv(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, 
     width, W, wp, bp = _conv_weights(x, weight, bias)
     xp, ld_x = _rows(x, lead, (width,), "x")
     sp = _flat(state_in, (seqs, W - 1, width), x.dtype, "state_in")
-    with _on(dev, stream, (x, weight, bias, state_in, cu_seqlens)) as handle:
+    ctx, handle = _on(dev, stream, (x, weight, bias, state_in, cu_seqlens))
+    with ctx:
         y = torch.empty((*lead, width), dtype=out_dtype or x.dtype, device=dev)
         state = (torch.empty((seqs, max(W - 1, 0), width), dtype=x.dtype, device=dev)
                  if want_state else None)
@@ -550,7 +545,8 @@ def short_conv_step(x, weight, bias, state, silu=True, out_dtype=None, stream=No
     seqs = x.shape[0]
     xp, ld_x = _rows(x, x.shape[:1], (width,), "x")
     sp = _flat(state, (seqs, W - 1, width), x.dtype, "state")
-    with _on(dev, stream, (x, weight, bias, state)) as handle:
+    ctx, handle = _on(dev, stream, (x, weight, bias, state))
+    with ctx:
         y = torch.empty((seqs, width), dtype=out_dtype or x.dtype, device=dev)
         _check("la_short_conv_step", lib().la_short_conv_step(
             xp, ld_x, wp, bp, sp, y.data_ptr() or None, seqs, width, W, 1 if silu else 0, _dt(x),
@@ -571,7 +567,8 @@ def short_conv_backward(dy, x, weight, bias=None, silu=True, state_in=None, dsta
     dyp, ld_dy = _rows(dy, lead, (width,), "dy")
     sp = _flat(state_in, (seqs, W - 1, width), x.dtype, "state_in")
     dsp = _flat(dstate_out, (seqs, W - 1, width), x.dtype, "dstate_out")
-    with _on(dev, stream, (dy, x, weight, bias, state_in, dstate_out, cu_seqlens)) as handle:
+    ctx, handle = _on(dev, stream, (dy, x, weight, bias, state_in, dstate_out, cu_seqlens))
+    with ctx:
         t = out_dtype or x.dtype
         out = {"dx": torch.empty((*lead, width), dtype=t, device=dev),
                "dweight": torch.empty((width, W), dtype=torch.float32, device=dev)}
@@ -602,7 +599,8 @@ def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, 
     wp = _flat(weight, (F,), torch.float32, "weight")
     bp = _flat(bias, (F,), torch.float32, "bias")
     rows = x.numel() // F if F else 0
-    with _on(dev, stream, (x, weight, bias)) as handle:
+    ctx, handle = _on(dev, stream, (x, weight, bias))
+    with ctx:
         y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
         mean = rstd = None
         if want_stats:
@@ -623,7 +621,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_bias=True, out_dtype=Non
     wp = _flat(weight, (F,), f32, "weight")
     mp, rp = _flat(mean, x.shape[:-1], f32, "mean"), _flat(rstd, x.shape[:-1], f32, "rstd")
     rows = x.numel() // F if F else 0
-    with _on(dev, stream, (dy, x, weight, mean, rstd)) as handle:
+    ctx, handle = _on(dev, stream, (dy, x, weight, mean, rstd))
+    with ctx:
         dx = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
         dw = torch.empty((F,), dtype=f32, device=dev)
         db = torch.empty((F,), dtype=f32, device=dev) if want_bias else None

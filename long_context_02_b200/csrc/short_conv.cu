@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(ConvArgs a)
 // over the tile's own rows and written as a partial sum. CTAs behind the tiles
 // write dstate_in: the rows before a sequence's first token.
 template <typename T, typename To, int W, int V>
-__global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
+__global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
 {
     constexpr int H = (V + 1) / 2;
     const int cb = blockIdx.x % a.cblocks;
@@ -374,39 +374,55 @@ __global__ void __launch_bounds__(NT) conv_backward_kernel(ConvArgs a)
         }
         const long long low = start > t0 ? start : t0;
         const int n = (int)(t - low + 1);
-        Row<T, V> xs[BACK_AHEAD], gs[BACK_AHEAD];
-        auto load = [&](int at) {
+        To* out = (To*)a.dx + t * a.D + c;
+        auto finish = [&](long long tok, To* to) {
+            f2 v[H];
+            pull(v);
+            if (dst && tok >= end - (W - 1)) from_state(tok, v);
+            store_row<To, V>(to, v);
 #pragma unroll
-            for (int k = 0; k < BACK_AHEAD; ++k) {
-                const long long tok = t - (at + k < n ? at + k : n - 1);
-                xs[k] = input(tok - (W - 1));
-                gs[k].load(dy + tok * a.ld_dy);
+            for (int i = 0; i < H; ++i) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][i] = fma2(q[0][i], win[j][i], dw[j][i]);
+                db[i] = add2(db[i], q[0][i]);
             }
         };
-        load(0);
+        // Whole groups of rows, so that the windows' shifts are a renaming of
+        // registers; then the rest one by one.
+        const int whole = n / BACK_AHEAD * BACK_AHEAD;
+        Row<T, V> xs[BACK_AHEAD], gs[BACK_AHEAD];
+        auto load = [&](long long tok) {
+            const T* xp = x + (tok - (W - 1)) * a.ld_x;
+            const T* gp = dy + tok * a.ld_dy;
+            if (tok - (BACK_AHEAD - 1) - (W - 1) >= start) {
+#pragma unroll
+                for (int k = 0; k < BACK_AHEAD; ++k) xs[k].load(xp - (long long)k * a.ld_x);
+            } else {
+#pragma unroll
+                for (int k = 0; k < BACK_AHEAD; ++k) xs[k] = input(tok - k - (W - 1));
+            }
+#pragma unroll
+            for (int k = 0; k < BACK_AHEAD; ++k) gs[k].load(gp - (long long)k * a.ld_dy);
+        };
+        if (whole) load(t);
 #pragma unroll 1
-        for (int at = 0; at < n; at += BACK_AHEAD) {
+        for (int at = 0; at < whole; at += BACK_AHEAD) {
             Row<T, V> xn[BACK_AHEAD], gn[BACK_AHEAD];
 #pragma unroll
             for (int k = 0; k < BACK_AHEAD; ++k) xn[k] = xs[k], gn[k] = gs[k];
-            if (at + BACK_AHEAD < n) load(at + BACK_AHEAD);
+            if (at + BACK_AHEAD < whole) load(t - at - BACK_AHEAD);
 #pragma unroll
             for (int k = 0; k < BACK_AHEAD; ++k) {
-                if (at + k < n) {
-                    const long long tok = t - at - k;
-                    step(xn[k], gn[k]);
-                    f2 v[H];
-                    pull(v);
-                    if (tok >= end - (W - 1)) from_state(tok, v);
-                    store_row<To, V>((To*)a.dx + tok * a.D + c, v);
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][i] = fma2(q[0][i], win[j][i], dw[j][i]);
-                        db[i] = add2(db[i], q[0][i]);
-                    }
-                }
+                step(xn[k], gn[k]);
+                finish(t - at - k, out - (long long)(at + k) * a.D);
             }
+        }
+#pragma unroll 1
+        for (int at = whole; at < n; ++at) {
+            Row<T, V> g;
+            g.load(dy + (t - at) * a.ld_dy);
+            step(input(t - at - (W - 1)), g);
+            finish(t - at, out - (long long)at * a.D);
         }
         t -= n;
     }

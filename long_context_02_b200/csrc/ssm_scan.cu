@@ -383,43 +383,83 @@ __global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanAr
 }
 
 // One token per sequence: the states are the traffic, one vector of four per
-// thread, read and written once.
-template <typename T, int K>
-__global__ void __launch_bounds__(256) scan_step_kernel(la_scan_inputs in, float* state, void* y,
-                                                        int B, int D, int G, int n, int out_f32)
+// thread and sequence, read and written once. A thread takes one channel of BB
+// sequences, for which it reads the weights once and whose loads it starts
+// together.
+constexpr int BB = 4;
+
+// Four of B or C at p (the thread's first is m0 of n).
+template <typename T> __device__ __forceinline__ void load_four(float* v, const T* p, int m0, int n, bool vec)
 {
-    constexpr int S = SCAN_S;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int m0 = (tid % K) * S;
-    const long long p = (long long)blockIdx.x * (256 / K) + tid / K;  // sequence * D + channel
-    const bool ok = p < (long long)B * D;
-    const int b = ok ? (int)(p / D) : 0, c = ok ? (int)(p % D) : 0, g = c / (D / G);
-    float h[S], A[S], acc = 0.f;
-    load_states(h, state + (ok ? p : 0) * n, m0, n);
-    load_states(A, in.A + (long long)c * n, m0, n);
-    const float u = to_f32(((const T*)in.u)[b * in.ld_u + c]);
-    float dt = to_f32(((const T*)in.delta)[b * in.ld_delta + c]);
-    const float z = in.z ? to_f32(((const T*)in.z)[b * in.ld_z + c]) : 0.f;
-    const T* Bp = (const T*)in.B + b * in.ld_b + (long long)g * n;
-    const T* Cp = (const T*)in.C + b * in.ld_c + (long long)g * n;
-    if (in.delta_bias) dt += in.delta_bias[c];
-    if (in.softplus) dt = softplus_f(dt);
+    if (vec) {
+        if constexpr (sizeof(T) == 2) {
+            const uint2 w = m0 < n ? *reinterpret_cast<const uint2*>(p + m0) : make_uint2(0, 0);
+            v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+            v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+            load_states(v, p, m0, n);
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const bool in_n = m0 + i < n;
-        const float bv = in_n ? to_f32(Bp[m0 + i]) : 0.f, cv = in_n ? to_f32(Cp[m0 + i]) : 0.f;
-        h[i] = fmaf(ex2(dt * (A[i] * SCAN_LOG2E)), h[i], dt * u * bv);
-        acc = fmaf(cv, h[i], acc);
+        for (int i = 0; i < 4; ++i) v[i] = m0 + i < n ? to_f32(p[m0 + i]) : 0.f;
+    }
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float* state, void* y,
+                                                        int B, int D, int G, int n, int cblocks,
+                                                        bool vec, int out_f32)
+{
+    constexpr int S = SCAN_S, CC = 128 / K;
+    const int tid = threadIdx.x, m0 = (tid % K) * S;
+    const int c_ = blockIdx.x % cblocks * CC + tid / K, b0 = blockIdx.x / cblocks * BB;
+    const bool c_ok = c_ < D;
+    const int c = c_ok ? c_ : D - 1, g = c / (D / G);
+    float h[BB][S], A[S], Bv[BB][S], Cv[BB][S];
+    T u[BB], d[BB], z[BB];
+#pragma unroll
+    for (int i = 0; i < BB; ++i) {
+        const long long b = min(b0 + i, B - 1);
+        load_states(h[i], state + (b * D + c) * n, m0, n);
+        u[i] = ((const T*)in.u)[b * in.ld_u + c];
+        d[i] = ((const T*)in.delta)[b * in.ld_delta + c];
+        if (in.z) z[i] = ((const T*)in.z)[b * in.ld_z + c];
+        load_four(Bv[i], (const T*)in.B + b * in.ld_b + (long long)g * n, m0, n, vec);
+        load_four(Cv[i], (const T*)in.C + b * in.ld_c + (long long)g * n, m0, n, vec);
+    }
+    load_states(A, in.A + (long long)c * n, m0, n);
+    const float bias = in.delta_bias ? in.delta_bias[c] : 0.f, Dw = in.D ? in.D[c] : 0.f;
+    f2 dt[BB / 2];
+#pragma unroll
+    for (int i = 0; i < BB; i += 2) {
+        dt[i / 2] = pack(to_f32(d[i]) + bias, to_f32(d[i + 1]) + bias);
+        if (in.softplus) dt[i / 2] = softplus2(dt[i / 2]);
     }
 #pragma unroll
-    for (int m = K / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-    if (!ok) return;
-    store_states(state + p * n, h, m0, n);
-    if (lane % K == 0) {
-        float v = in.D ? fmaf(in.D[c], u, acc) : acc;
-        if (in.z) v *= z * sigmoid_f(z);
-        if (out_f32) ((float*)y)[p] = v;
-        else ((__nv_bfloat16*)y)[p] = __float2bfloat16_rn(v);
+    for (int i = 0; i < BB; ++i) {
+        float lo, hi;
+        unpack(dt[i / 2], lo, hi);
+        const float t = i % 2 ? hi : lo, uu = to_f32(u[i]), tu = t * uu;
+        float acc = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            h[i][s] = fmaf(ex2(t * (A[s] * SCAN_LOG2E)), h[i][s], tu * Bv[i][s]);
+            acc = fmaf(Cv[i][s], h[i][s], acc);
+        }
+#pragma unroll
+        for (int m = K / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+        if (!c_ok || b0 + i >= B) continue;
+        const long long p = (long long)(b0 + i) * D + c;
+        store_states(state + p * n, h[i], m0, n);
+        if (tid % K == 0) {
+            float v = fmaf(Dw, uu, acc);
+            if (in.z) {
+                const float zz = to_f32(z[i]);
+                v *= zz * sigmoid_f(zz);
+            }
+            if (out_f32) ((float*)y)[p] = v;
+            else ((__nv_bfloat16*)y)[p] = __float2bfloat16_rn(v);
+        }
     }
 }
 
@@ -603,16 +643,22 @@ cudaError_t launch_scan(const ScanProblem& p, const float* state_in, void* y, fl
 
 cudaError_t launch_scan_step(const ScanProblem& p, float* state, void* y, cudaStream_t stream)
 {
-    const int K = scan_lanes(p.n), CC = 256 / K, B = p.view.num_seqs;
-    const unsigned grid = (unsigned)(((long long)B * p.D + CC - 1) / CC);
+    const int K = scan_lanes(p.n), CC = 128 / K, B = p.view.num_seqs;
+    const int cblocks = (p.D + CC - 1) / CC;
+    const unsigned grid = (unsigned)((long long)cblocks * ((B + BB - 1) / BB));
+    const size_t four = p.in_t == LA_BF16 ? 8 : 16;  // bytes of four of B or C
+    const auto fours = [&](const void* q, long long ld) {
+        return (uintptr_t)q % four == 0 && ld % 4 == 0;
+    };
+    const bool vec = p.n % 4 == 0 && fours(p.in.B, p.in.ld_b) && fours(p.in.C, p.in.ld_c);
+    const int f32 = p.out_t == LA_F32;
 #define LA_CALL(KK)                                                                              \
     if (p.in_t == LA_BF16)                                                                       \
-        scan_step_kernel<__nv_bfloat16, KK><<<grid, 256, 0, stream>>>(p.in, state, y, B, p.D,    \
-                                                                      p.G, p.n,                  \
-                                                                      p.out_t == LA_F32);        \
+        scan_step_kernel<__nv_bfloat16, KK>                                                      \
+            <<<grid, 128, 0, stream>>>(p.in, state, y, B, p.D, p.G, p.n, cblocks, vec, f32);     \
     else                                                                                         \
-        scan_step_kernel<float, KK><<<grid, 256, 0, stream>>>(p.in, state, y, B, p.D, p.G, p.n,  \
-                                                              1);
+        scan_step_kernel<float, KK>                                                              \
+            <<<grid, 128, 0, stream>>>(p.in, state, y, B, p.D, p.G, p.n, cblocks, vec, f32);
     LA_SCAN_DISPATCH_K(p.n, LA_CALL)
 #undef LA_CALL
     count_launch();
