@@ -385,7 +385,9 @@ __global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanAr
 // One token per sequence: the states are the traffic, one vector of four per
 // thread and sequence, read and written once. A thread takes one channel of BB
 // sequences, for which it reads the weights once and whose loads it starts
-// together.
+// together. What depends on the channel alone is shared out: each of the
+// channel's K lanes makes dt, dt u and the gate of BB / K sequences, passes the
+// former on, and finishes the output of the same ones.
 constexpr int BB = 4;
 
 // Four of B or C at p (the thread's first is m0 of n).
@@ -411,55 +413,74 @@ __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float
                                                         bool vec, int out_f32)
 {
     constexpr int S = SCAN_S, CC = 128 / K;
-    const int tid = threadIdx.x, m0 = (tid % K) * S;
+    constexpr int EL = K < BB ? BB / K : 1;  // sequences whose elements a lane makes
+    const int tid = threadIdx.x, lane = tid & 31, m0 = (tid % K) * S;
     const int c_ = blockIdx.x % cblocks * CC + tid / K, b0 = blockIdx.x / cblocks * BB;
     const bool c_ok = c_ < D;
-    const int c = c_ok ? c_ : D - 1, g = c / (D / G);
+    const int c = c_ok ? c_ : D - 1, g = G == 1 ? 0 : c / (D / G);
     float h[BB][S], A[S], Bv[BB][S], Cv[BB][S];
-    T u[BB], d[BB], z[BB];
+    const float* hp = state + ((long long)b0 * D + c) * n;
 #pragma unroll
     for (int i = 0; i < BB; ++i) {
-        const long long b = min(b0 + i, B - 1);
-        load_states(h[i], state + (b * D + c) * n, m0, n);
-        u[i] = ((const T*)in.u)[b * in.ld_u + c];
-        d[i] = ((const T*)in.delta)[b * in.ld_delta + c];
-        if (in.z) z[i] = ((const T*)in.z)[b * in.ld_z + c];
-        load_four(Bv[i], (const T*)in.B + b * in.ld_b + (long long)g * n, m0, n, vec);
-        load_four(Cv[i], (const T*)in.C + b * in.ld_c + (long long)g * n, m0, n, vec);
+        const long long b = min(b0 + i, B - 1) - b0;
+        load_states(h[i], hp + b * D * n, m0, n);
+    }
+    const int mine = b0 + reduced_index<BB, K, 1>(lane);
+    float u[EL], d[EL], z[EL];
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+        const long long b = min(mine + e, B - 1);
+        u[e] = to_f32(((const T*)in.u)[b * in.ld_u + c]);
+        d[e] = to_f32(((const T*)in.delta)[b * in.ld_delta + c]);
+        z[e] = in.z ? to_f32(((const T*)in.z)[b * in.ld_z + c]) : 0.f;
+    }
+    const T* Bp = (const T*)in.B + b0 * in.ld_b + (long long)g * n;
+    const T* Cp = (const T*)in.C + b0 * in.ld_c + (long long)g * n;
+#pragma unroll
+    for (int i = 0; i < BB; ++i) {
+        const long long b = min(b0 + i, B - 1) - b0;
+        load_four(Bv[i], Bp + b * in.ld_b, m0, n, vec);
+        load_four(Cv[i], Cp + b * in.ld_c, m0, n, vec);
     }
     load_states(A, in.A + (long long)c * n, m0, n);
-    const float bias = in.delta_bias ? in.delta_bias[c] : 0.f, Dw = in.D ? in.D[c] : 0.f;
-    f2 dt[BB / 2];
 #pragma unroll
-    for (int i = 0; i < BB; i += 2) {
-        dt[i / 2] = pack(to_f32(d[i]) + bias, to_f32(d[i + 1]) + bias);
-        if (in.softplus) dt[i / 2] = softplus2(dt[i / 2]);
+    for (int s = 0; s < S; ++s) A[s] *= SCAN_LOG2E;
+    const float bias = in.delta_bias ? in.delta_bias[c] : 0.f;
+    float acc[BB];
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+        d[e] += bias;
+        if (in.softplus) d[e] = softplus_f(d[e]);
     }
 #pragma unroll
     for (int i = 0; i < BB; ++i) {
-        float lo, hi;
-        unpack(dt[i / 2], lo, hi);
-        const float t = i % 2 ? hi : lo, uu = to_f32(u[i]), tu = t * uu;
-        float acc = 0.f;
+        constexpr int PER = K > BB ? K / BB : 1;  // lanes with the same sequence
+        const int from = (lane & ~(K - 1)) + (K > BB ? i * PER : i / EL);
+        const float dt = __shfl_sync(0xffffffffu, d[i % EL], from);
+        const float du = dt * __shfl_sync(0xffffffffu, u[i % EL], from);
+        acc[i] = 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            h[i][s] = fmaf(ex2(t * (A[s] * SCAN_LOG2E)), h[i][s], tu * Bv[i][s]);
-            acc = fmaf(Cv[i][s], h[i][s], acc);
+            h[i][s] = fmaf(ex2(dt * A[s]), h[i][s], du * Bv[i][s]);
+            acc[i] = fmaf(Cv[i][s], h[i][s], acc[i]);
         }
+    }
+    lane_reduce<BB, K, 1>(acc, lane);
+    if (!c_ok) return;
+    float* hq = state + ((long long)b0 * D + c) * n;
 #pragma unroll
-        for (int m = K / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-        if (!c_ok || b0 + i >= B) continue;
-        const long long p = (long long)(b0 + i) * D + c;
-        store_states(state + p * n, h[i], m0, n);
-        if (tid % K == 0) {
-            float v = fmaf(Dw, uu, acc);
-            if (in.z) {
-                const float zz = to_f32(z[i]);
-                v *= zz * sigmoid_f(zz);
-            }
-            if (out_f32) ((float*)y)[p] = v;
-            else ((__nv_bfloat16*)y)[p] = __float2bfloat16_rn(v);
-        }
+    for (int i = 0; i < BB; ++i)
+        if (b0 + i < B) store_states(hq + (long long)i * D * n, h[i], m0, n);
+    if (!reduced_writer<BB, K, 1>(lane)) return;
+    const float Dw = in.D ? in.D[c] : 0.f;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+        if (mine + e >= B) continue;
+        float v = fmaf(Dw, u[e], acc[e]);
+        if (in.z) v *= z[e] * sigmoid_f(z[e]);
+        const long long p = (long long)(mine + e) * D + c;
+        if (out_f32) ((float*)y)[p] = v;
+        else ((__nv_bfloat16*)y)[p] = __float2bfloat16_rn(v);
     }
 }
 

@@ -381,7 +381,8 @@ def test_offsets_beyond_32_bits():
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,F", [(1, 1), (1, 8), (5, 7), (33, 64), (7, 513), (3, 1024), (9, 1025), (5, 2048),
-                                    (300, 2056), (4, 4100), (3, 8192), (2, 8191), (4, 16384), (2, 16383)])
+                                    (300, 2056), (4, 4100), (3, 8192), (2, 8191), (4, 16384), (2, 16383),
+                                    (1300, 1032), (1187, 2056), (1185, 4104), (1186, 8200), (1200, 1031)])
 def test_layer_norm(rows, F, dtype):
     g = torch.Generator().manual_seed(rows + F)
     x = (_rnd(g, rows, F) + 3).to(dtype)
