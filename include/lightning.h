@@ -450,7 +450,8 @@ LA_API int la_short_conv_backward(const int* cu_seqlens, int num_seqs, const voi
  *   weight      in   [F] fp32; bias [F] fp32 or NULL
  *   eps         in   >= 0 and finite
  *   y           out  [rows][F], dtype out_t; may be x when the dtypes are the same
- *   mean, rstd  out  [rows] fp32, what the backward call takes; both or neither NULL
+ *   mean, rstd  out  [rows] fp32, 4-byte aligned, what the backward call takes; both or
+ *                    neither NULL
  * rows may be 0. No workspace.
  */
 LA_API int la_layer_norm(const void* x, const float* weight, const float* bias, float eps,
@@ -461,7 +462,7 @@ LA_API int la_layer_norm(const void* x, const float* weight, const float* bias, 
  * Gradients of the layer norm: with v = (x - mean) rstd and e = dy weight,
  *     dx = rstd (e - mean_f e - v mean_f(e v)),  dweight = sum_rows dy v,  dbias = sum_rows dy
  *   dy, x       in   [rows][F], dtype in_t
- *   mean, rstd  in   [rows] fp32 from the forward call
+ *   mean, rstd  in   [rows] fp32, 4-byte aligned, from the forward call
  *   dx          out  [rows][F], dtype out_t
  *   dweight     out  [F] fp32; dbias [F] fp32 or NULL
  *   workspace   at least la_workspace_bytes(LA_OP_NORM_BACKWARD, ...) bytes

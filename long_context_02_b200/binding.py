@@ -604,8 +604,7 @@ def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, 
         y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
         mean = rstd = None
         if want_stats:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-            rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
         _check("la_layer_norm", lib().la_layer_norm(
             xp, wp, bp, eps, y.data_ptr() or None, mean.data_ptr() or None if want_stats else None,
             rstd.data_ptr() or None if want_stats else None, rows, F, _dt(x), _dt(y), handle))

@@ -13,8 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblightning.so")
 SOURCES = ["api.cu", "simt_forward.cu", "decode.cu", "tc_forward.cu", "noalloc.cu",
-           "norm_gate.cu", "lasp.cu", "ssm_api.cu", "ssm_scan.cu", "ssm_scan_backward.cu",
-           "short_conv.cu", "layer_norm.cu"]
+           "norm_gate.cu", "lasp.cu", "ssm_api.cu", "ssm_common.cu", "ssm_scan.cu",
+           "ssm_scan_backward.cu", "short_conv.cu", "layer_norm.cu"]
 HEADERS = ["common.cuh", "kernels.h", "tc_forward.h", "ssm.h", "ssm_scan.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

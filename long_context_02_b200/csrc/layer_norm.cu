@@ -14,6 +14,8 @@
 namespace la {
 namespace {
 
+constexpr int MOST_SHARED = 200 * 1024;  // of dynamic shared memory that a ring asks for
+
 // From so many rows on the forward pass walks them through shared memory.
 constexpr long long LA_RING_ROWS = 148 * 8;
 
@@ -639,7 +641,7 @@ cudaError_t launch_ring(const void* x, const float* weight, const float* bias, f
     constexpr int R = sizeof(T) == 2 ? (NT > 512 ? 2 : 4) : (NT > 512 ? 1 : 2), STAGES = 3;
     auto kernel = norm_ring_kernel<T, To, NT, V, 16 / V, STAGES, R>;
     const int smem = STAGES * R * F * (int)sizeof(T);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_shared((const void*)kernel, MOST_SHARED);
     if (e != cudaSuccess) return e;
     const long long sets = (rows + R - 1) / R, most = 148 * (NT < 512 ? 512 / NT : 1);
     kernel<<<(unsigned)(sets < most ? sets : most), NT, smem, stream>>>(
@@ -718,8 +720,7 @@ cudaError_t launch_backward(const void* dy, const void* x, const float* weight, 
     auto kernel = norm_backward_kernel<T, To, NT, V, CH, STAGES, R>;
     const int smem = STAGES > 1 ? STAGES * R * 2 * F * (int)sizeof(T) : 0;
     if (smem > 40 * 1024) {  // beside the static slots of the sums
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+        cudaError_t e = allow_shared((const void*)kernel, MOST_SHARED);
         if (e != cudaSuccess) return e;
     }
     kernel<<<ctas, NT, smem, stream>>>((const T*)dy, (const T*)x, weight, mean, rstd, (To*)dx, dw,
@@ -745,9 +746,10 @@ cudaError_t launch_layer_norm_backward(const void* dy, const void* x, const floa
         count_launch();
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_column_sum(dw, dweight, ctas, F, stream);
-    if (e == cudaSuccess && dbias) e = launch_column_sum(db, dbias, ctas, F, stream);
-    return e;
+    SumJobs sums;
+    sums.add(dw, dweight, ctas, F);
+    sums.add(db, dbias, ctas, F);
+    return launch_column_sums(sums, stream);
 }
 
 }  // namespace la

@@ -14,8 +14,6 @@ namespace la {
 namespace {
 
 constexpr int NT = 128;
-constexpr int TILE = 64;        // tokens per thread, forward
-constexpr int BACK_TILE = 128;  // tokens per thread, backward
 constexpr int AHEAD = 8;        // rows in flight per thread while the rows before them are used
 constexpr int BACK_AHEAD = 4;   // the same, backward (two rows each)
 
@@ -29,6 +27,7 @@ struct ConvArgs {
     void* state_out;
     SeqView view;
     int D, silu, cblocks;
+    int tile;  // rows per CTA
     long long tiles;
     // backward
     const void* dy;
@@ -151,8 +150,8 @@ __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a)
     }
     f2 w[W][H], b[H];
     load_weights<W, V>(a.weight, a.bias, c, w, b);
-    const long long t0 = tile * TILE;
-    const long long t1 = t0 + TILE < a.view.total ? t0 + TILE : a.view.total;
+    const long long t0 = tile * a.tile;
+    const long long t1 = t0 + a.tile < a.view.total ? t0 + a.tile : a.view.total;
     int s = a.view.find(t0);
     if (s >= a.view.num_seqs) return;
 
@@ -349,8 +348,8 @@ __global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
         return;
     }
 
-    const long long t0 = tile * BACK_TILE;
-    long long t1 = t0 + BACK_TILE < a.view.total ? t0 + BACK_TILE : a.view.total;
+    const long long t0 = tile * a.tile;
+    long long t1 = t0 + a.tile < a.view.total ? t0 + a.tile : a.view.total;
     // The sequence of the last row that has one.
     s = a.view.find(t1 - 1);
     if (s >= a.view.num_seqs) {
@@ -471,6 +470,18 @@ bool on_vectors(const void* p, long long ld, size_t e)
     else if (p.W == 3) { LA_CONV_TYPES(F, 3) }                                                   \
     else { LA_CONV_TYPES(F, 4) }
 
+// Rows per CTA: as many as make the CTAs a whole number of full waves of about
+// `about` rows (`resident` CTAs run at once), at least 16.
+int tile_rows(long long total, int cblocks, int resident, int about)
+{
+    const long long rows = total * cblocks;
+    long long waves = (rows + (long long)resident * about / 2) / ((long long)resident * about);
+    if (waves < 1) waves = 1;
+    const long long t = (rows + resident * waves - 1) / (resident * waves);
+    return (int)(t < 16 ? 16 : t);
+}
+constexpr int BACK_RESIDENT = 148 * 4, BACK_ABOUT = 128;
+
 ConvArgs base_args(const ConvProblem& p, bool vec)
 {
     ConvArgs a{};
@@ -501,7 +512,9 @@ cudaError_t launch_short_conv(const ConvProblem& p, const void* state_in, void* 
     a.state_in = state_in;
     a.y = y;
     a.state_out = state_out;
-    a.tiles = (p.view.total + TILE - 1) / TILE;
+    const long long rows = p.view.total * a.cblocks;
+    a.tile = rows >= 148 * 8 * 64 ? 64 : rows >= 148 * 8 * 32 ? 32 : 16;  // fill the SMs
+    a.tiles = (p.view.total + a.tile - 1) / a.tile;
     const long long grid = (a.tiles + (state_out ? p.view.num_seqs : 0)) * a.cblocks;
     if (grid == 0) return cudaSuccess;
 #define LA_CALL(T, To, W, V) conv_kernel<T, To, W, V><<<(unsigned)grid, NT, 0, stream>>>(a)
@@ -528,7 +541,12 @@ cudaError_t launch_short_conv_step(const ConvProblem& p, void* state, void* y,
 
 size_t conv_backward_workspace(int D, long long total, int W)
 {
-    const size_t tiles = (size_t)((total + BACK_TILE - 1) / BACK_TILE);
+    size_t tiles = 0;  // whichever number of channels a thread takes
+    for (int V : {1, 4}) {
+        const int tile = tile_rows(total, (D + NT * V - 1) / (NT * V), BACK_RESIDENT, BACK_ABOUT);
+        const size_t n = (size_t)((total + tile - 1) / tile);
+        tiles = n > tiles ? n : tiles;
+    }
     return align_up(tiles * D * W * 4, 256) + align_up(tiles * D * 4, 256);
 }
 
@@ -545,7 +563,8 @@ cudaError_t launch_short_conv_backward(const ConvProblem& p, const void* dy, lon
     a.dstate_out = dstate_out;
     a.dx = dx;
     a.dstate_in = dstate_in;
-    a.tiles = (p.view.total + BACK_TILE - 1) / BACK_TILE;
+    a.tile = tile_rows(p.view.total, a.cblocks, BACK_RESIDENT, BACK_ABOUT);
+    a.tiles = (p.view.total + a.tile - 1) / a.tile;
     a.dw_part = (float*)ws;
     a.db_part = (float*)((char*)ws + align_up((size_t)a.tiles * p.D * p.W * 4, 256));
     const long long grid = (a.tiles + (dstate_in ? p.view.num_seqs : 0)) * a.cblocks;
@@ -557,10 +576,10 @@ cudaError_t launch_short_conv_backward(const ConvProblem& p, const void* dy, lon
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_column_sum(a.dw_part, dweight, (int)a.tiles, (long long)p.D * p.W, stream);
-    if (e == cudaSuccess && dbias)
-        e = launch_column_sum(a.db_part, dbias, (int)a.tiles, p.D, stream);
-    return e;
+    SumJobs sums;
+    sums.add(a.dw_part, dweight, (int)a.tiles, (long long)p.D * p.W);
+    sums.add(a.db_part, dbias, (int)a.tiles, p.D);
+    return launch_column_sums(sums, stream);
 }
 
 }  // namespace la

@@ -67,9 +67,31 @@ struct Chunks {
 cudaError_t launch_plan_chunks(const SeqView& v, long long len, int items, int* first, int* seq_of,
                                cudaStream_t stream);
 
-// out[c] = sum over r of in[r][c], in a fixed order.
-cudaError_t launch_column_sum(const float* in, float* out, int rows, long long cols,
-                              cudaStream_t stream);
+// Column sums out[c] = sum over r < rows of in[r][c], in a fixed order, of up to
+// five matrices in one launch. Jobs without an output are left out.
+struct SumJobs {
+    struct Job {
+        const float* in;
+        void* out;
+        int rows;
+        long long cols;
+        int bf16;  // dtype of out
+        // Packed batch: only the columns of rows that a sequence holds, cu_end[0]
+        // times `per_row` of them; the others are left as they were.
+        const int* cu_end;
+        long long per_row;
+        long long first_block;
+        int strands;  // threads that share a column's rows
+    } job[5];
+    int count = 0;
+    long long blocks = 0;
+    void add(const float* in, void* out, int rows, long long cols, int bf16 = 0,
+             const int* cu_end = nullptr, long long per_row = 1);
+};
+cudaError_t launch_column_sums(const SumJobs& jobs, cudaStream_t stream);
+
+// Dynamic shared memory beyond the default limit, once per kernel and device.
+cudaError_t allow_shared(const void* kernel, int bytes);
 
 size_t ssm_workspace_bytes(int op, int G, int D, long long total, int n, int num_seqs);
 

@@ -285,7 +285,7 @@ LA_API int la_layer_norm(const void* x, const float* weight, const float* bias, 
     if (!(eps >= 0.f) || eps > 3.0e38f) return LA_ERR_INVALID_ARG;  // also rejects NaN
     if (rows == 0) return LA_OK;
     if (!y || !mean != !rstd || (y == x && in_t != out_t)) return LA_ERR_INVALID_ARG;
-    if (!aligned16(y) || !aligned16(mean) || !aligned16(rstd)) return LA_ERR_INVALID_ARG;
+    if (!aligned16(y) || !aligned(mean, 4) || !aligned(rstd, 4)) return LA_ERR_INVALID_ARG;
     return status_of(launch_layer_norm(x, weight, bias, eps, y, mean, rstd, rows, F, in_t, out_t,
                                        stream_of(stream)));
 }
@@ -299,7 +299,7 @@ LA_API int la_layer_norm_backward(const void* dy, const void* x, const float* we
     int st = check_norm(x, weight, dbias, rows, F, in_t, out_t);
     if (st != LA_OK) return st;
     if (!dweight || (rows > 0 && (!dy || !mean || !rstd || !dx))) return LA_ERR_INVALID_ARG;
-    if (!aligned16(dy) || !aligned16(mean) || !aligned16(rstd) || !aligned16(dx) ||
+    if (!aligned16(dy) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned16(dx) ||
         !aligned16(dweight))
         return LA_ERR_INVALID_ARG;
     if ((st = check_ws(workspace, ws_bytes, norm_backward_workspace(rows, F))) != LA_OK) return st;

@@ -391,15 +391,17 @@ __global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanAr
 constexpr int BB = 4;
 
 // Four of B or C at p (the thread's first is m0 of n).
-template <typename T> __device__ __forceinline__ void load_four(float* v, const T* p, int m0, int n, bool vec)
+template <typename T, bool FULL>
+__device__ __forceinline__ void load_four(float* v, const T* p, int m0, int n, bool vec)
 {
-    if (vec) {
+    if (FULL || vec) {
         if constexpr (sizeof(T) == 2) {
-            const uint2 w = m0 < n ? *reinterpret_cast<const uint2*>(p + m0) : make_uint2(0, 0);
+            const uint2 w = FULL || m0 < n ? *reinterpret_cast<const uint2*>(p + m0)
+                                           : make_uint2(0, 0);
             v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
             v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
         } else {
-            load_states(v, p, m0, n);
+            load_states<FULL>(v, p, m0, n);
         }
     } else {
 #pragma unroll
@@ -407,7 +409,8 @@ template <typename T> __device__ __forceinline__ void load_four(float* v, const 
     }
 }
 
-template <typename T, int K>
+// FULL: n = 4 K, and B and C are on vectors of four.
+template <typename T, int K, bool FULL>
 __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float* state, void* y,
                                                         int B, int D, int G, int n, int cblocks,
                                                         bool vec, int out_f32)
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float
 #pragma unroll
     for (int i = 0; i < BB; ++i) {
         const long long b = min(b0 + i, B - 1) - b0;
-        load_states(h[i], hp + b * D * n, m0, n);
+        load_states<FULL>(h[i], hp + b * D * n, m0, n);
     }
     const int mine = b0 + reduced_index<BB, K, 1>(lane);
     float u[EL], d[EL], z[EL];
@@ -439,10 +442,10 @@ __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float
 #pragma unroll
     for (int i = 0; i < BB; ++i) {
         const long long b = min(b0 + i, B - 1) - b0;
-        load_four(Bv[i], Bp + b * in.ld_b, m0, n, vec);
-        load_four(Cv[i], Cp + b * in.ld_c, m0, n, vec);
+        load_four<T, FULL>(Bv[i], Bp + b * in.ld_b, m0, n, vec);
+        load_four<T, FULL>(Cv[i], Cp + b * in.ld_c, m0, n, vec);
     }
-    load_states(A, in.A + (long long)c * n, m0, n);
+    load_states<FULL>(A, in.A + (long long)c * n, m0, n);
 #pragma unroll
     for (int s = 0; s < S; ++s) A[s] *= SCAN_LOG2E;
     const float bias = in.delta_bias ? in.delta_bias[c] : 0.f;
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float
     float* hq = state + ((long long)b0 * D + c) * n;
 #pragma unroll
     for (int i = 0; i < BB; ++i)
-        if (b0 + i < B) store_states(hq + (long long)i * D * n, h[i], m0, n);
+        if (b0 + i < B) store_states<FULL>(hq + (long long)i * D * n, h[i], m0, n);
     if (!reduced_writer<BB, K, 1>(lane)) return;
     const float Dw = in.D ? in.D[c] : 0.f;
 #pragma unroll
@@ -564,8 +567,7 @@ cudaError_t launch_tiles(void (*states)(ScanArgs), void (*outputs)(ScanArgs), co
     constexpr int smem = 2 * (int)sizeof(ScanTile<K>);
     for (auto kernel : {cut ? states : nullptr, outputs}) {
         if (!kernel) continue;
-        cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = allow_shared((const void*)kernel, smem);
         if (e != cudaSuccess) return e;
         kernel<<<grid, NT + SV, smem, stream>>>(a);
         count_launch();
@@ -673,15 +675,20 @@ cudaError_t launch_scan_step(const ScanProblem& p, float* state, void* y, cudaSt
     };
     const bool vec = p.n % 4 == 0 && fours(p.in.B, p.in.ld_b) && fours(p.in.C, p.in.ld_c);
     const int f32 = p.out_t == LA_F32;
+#define LA_STEP(T, KK, FULL)                                                                     \
+    scan_step_kernel<T, KK, FULL><<<grid, 128, 0, stream>>>(p.in, state, y, B, p.D, p.G, p.n,    \
+                                                            cblocks, vec, f32)
 #define LA_CALL(KK)                                                                              \
-    if (p.in_t == LA_BF16)                                                                       \
-        scan_step_kernel<__nv_bfloat16, KK>                                                      \
-            <<<grid, 128, 0, stream>>>(p.in, state, y, B, p.D, p.G, p.n, cblocks, vec, f32);     \
-    else                                                                                         \
-        scan_step_kernel<float, KK>                                                              \
-            <<<grid, 128, 0, stream>>>(p.in, state, y, B, p.D, p.G, p.n, cblocks, vec, f32);
+    if (vec && p.n == SCAN_S * KK) {                                                             \
+        if (p.in_t == LA_BF16) LA_STEP(__nv_bfloat16, KK, true);                                 \
+        else LA_STEP(float, KK, true);                                                           \
+    } else {                                                                                     \
+        if (p.in_t == LA_BF16) LA_STEP(__nv_bfloat16, KK, false);                                \
+        else LA_STEP(float, KK, false);                                                          \
+    }
     LA_SCAN_DISPATCH_K(p.n, LA_CALL)
 #undef LA_CALL
+#undef LA_STEP
     count_launch();
     return cudaGetLastError();
 }

@@ -222,21 +222,24 @@ template <bool VEC> struct Pair<float, VEC> {
 };
 
 // Four states of one channel at p (n of them in all, this thread's start at
-// m0); vectors when a row of n states keeps 16-byte alignment.
+// m0); vectors when a row of n states keeps 16-byte alignment. FULL: n is known
+// to be a multiple of four above m0.
+template <bool FULL = false>
 __device__ __forceinline__ void load_states(float* v, const float* p, int m0, int n)
 {
-    if ((n & 3) == 0) {
-        const float4 x = m0 < n ? *reinterpret_cast<const float4*>(p + m0) : make_float4(0, 0, 0, 0);
+    if (FULL || (n & 3) == 0) {
+        const float4 x = FULL || m0 < n ? *reinterpret_cast<const float4*>(p + m0) : make_float4(0, 0, 0, 0);
         v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = m0 + i < n ? p[m0 + i] : 0.f;
     }
 }
+template <bool FULL = false>
 __device__ __forceinline__ void store_states(float* p, const float* v, int m0, int n)
 {
-    if ((n & 3) == 0) {
-        if (m0 < n) *reinterpret_cast<float4*>(p + m0) = make_float4(v[0], v[1], v[2], v[3]);
+    if (FULL || (n & 3) == 0) {
+        if (FULL || m0 < n) *reinterpret_cast<float4*>(p + m0) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

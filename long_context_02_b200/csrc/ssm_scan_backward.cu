@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(NT, 3) main_kernel(BackArgs a)
         struct {
             float v[8];
             f2 gB, gA, y;
-        } last;
+        } last = {};
         auto flush = [&](int q) {
             sh.gB[q][tid] = last.gB;
             sh.gA[q][tid] = last.gA;
@@ -604,44 +604,6 @@ __global__ void __launch_bounds__(NT, 3) main_kernel(BackArgs a)
     }
 }
 
-// dB and dC: the sum of the channel blocks' slabs, for the rows of a sequence.
-__global__ void __launch_bounds__(256) sum_bc_kernel(BackArgs a)
-{
-    const long long cols = (long long)a.G * a.n;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long rows = a.view.cu ? a.view.cu[a.view.num_seqs] : a.view.total;
-    if (i >= a.view.total * cols || i / cols >= rows) return;
-    const long long slab = a.view.total * cols;
-    const float* in = (blockIdx.y ? a.dCp : a.dBp) + i;
-    float v = 0.f;
-#pragma unroll 8
-    for (int r = 0; r < a.cpg; ++r) v += in[r * slab];
-    void* out = blockIdx.y ? a.out.dC : a.out.dB;
-    if (a.out_f32) ((float*)out)[i] = v;
-    else ((__nv_bfloat16*)out)[i] = __float2bfloat16_rn(v);
-}
-
-// out[c] = sum of in[r][c]: 32 columns per CTA, 32 strands of rows.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* in, float* out,
-                                                          int rows, long long cols)
-{
-    __shared__ float part[32][33];
-    const int x = threadIdx.x, y = threadIdx.y;
-    const long long c = (long long)blockIdx.x * 32 + x;
-    float v = 0.f;
-    if (c < cols) {
-#pragma unroll 4
-        for (int r = y; r < rows; r += 32) v += in[r * cols + c];
-    }
-    part[y][x] = v;
-    __syncthreads();
-    v = part[x][y];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const long long oc = (long long)blockIdx.x * 32 + y;
-    if (x == 0 && oc < cols) out[oc] = v;
-}
-
 // Lanes per pair of channels.
 int back_lanes(int n)
 {
@@ -690,15 +652,6 @@ BackLayout back_layout(int G, int D, long long total, int n, int num_seqs)
 size_t scan_backward_workspace(int G, int D, long long total, int n, int num_seqs)
 {
     return back_layout(G, D, total, n, num_seqs).bytes;
-}
-
-cudaError_t launch_column_sum(const float* in, float* out, int rows, long long cols,
-                              cudaStream_t stream)
-{
-    column_sum_kernel<<<(unsigned)((cols + 31) / 32), dim3(32, 32), 0, stream>>>(in, out, rows,
-                                                                                cols);
-    count_launch();
-    return cudaGetLastError();
 }
 
 cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, const void* dy,
@@ -761,7 +714,7 @@ cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, co
         auto local = vec ? local_kernel<T, KK, true> : local_kernel<T, KK, false>;               \
         auto main = vec ? main_kernel<T, KK, true> : main_kernel<T, KK, false>;                  \
         const int smem = (int)sizeof(MainShared<KK>);                                            \
-        e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);       \
+        e = allow_shared((const void*)main, smem);                                               \
         if (e != cudaSuccess) return e;                                                          \
         local<<<grid, NT, 0, stream>>>(a);                                                       \
         combine_kernel<<<combine_grid, 128, 0, stream>>>(a, state_in, dstate_out);               \
@@ -780,18 +733,19 @@ cudaError_t launch_scan_backward(const ScanProblem& p, const float* state_in, co
 #undef LA_TYPE
         count_launch(3);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if (p.view.total > 0) {
-            const long long cells = p.view.total * p.G * p.n;
-            sum_bc_kernel<<<dim3((unsigned)((cells + 255) / 256), 2), 256, 0, stream>>>(a);
-            count_launch();
-        }
     }
-    const int rows = num_seqs > 0 ? a.ch.items : 0;
-    if ((e = launch_column_sum(a.hs, out.dA, rows, DN, stream)) != cudaSuccess) return e;
-    if (out.dD && (e = launch_column_sum(a.dDp, out.dD, rows, p.D, stream)) != cudaSuccess)
-        return e;
-    if (out.ddelta_bias) return launch_column_sum(a.dbp, out.ddelta_bias, rows, p.D, stream);
-    return cudaSuccess;
+    const int rows = num_seqs > 0 ? a.ch.items : 0, bf16 = !a.out_f32;
+    const long long cells = p.view.total * p.G * p.n;
+    const int* held = p.view.cu ? p.view.cu + num_seqs : nullptr;
+    SumJobs sums;
+    if (num_seqs > 0) {
+        sums.add(a.dBp, out.dB, a.cpg, cells, bf16, held, (long long)p.G * p.n);
+        sums.add(a.dCp, out.dC, a.cpg, cells, bf16, held, (long long)p.G * p.n);
+    }
+    sums.add(a.hs, out.dA, rows, DN);
+    sums.add(a.dDp, out.dD, rows, p.D);
+    sums.add(a.dbp, out.ddelta_bias, rows, p.D);
+    return launch_column_sums(sums, stream);
 }
 
 }  // namespace la
