@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -37,18 +38,9 @@ EXPORTED = ["la_workspace_bytes", "la_prefill", "la_prefill_varlen", "la_decode"
 _lib = None
 
 
-class ScanInputs(ctypes.Structure):
-    """la_scan_inputs of include/lightning.h."""
-    _fields_ = ([(f, ctypes.c_void_p) for f in ("u", "delta", "z", "B", "C")]
-                + [(f, ctypes.c_longlong) for f in ("ld_u", "ld_delta", "ld_z", "ld_b", "ld_c")]
-                + [(f, ctypes.c_void_p) for f in ("A", "D", "delta_bias")]
-                + [("softplus", ctypes.c_int)])
-
-
-class ScanGrads(ctypes.Structure):
-    """la_scan_grads of include/lightning.h."""
-    _fields_ = [(f, ctypes.c_void_p) for f in ("du", "ddelta", "dz", "dB", "dC", "dA", "dD",
-                                               "ddelta_bias", "dstate_in")]
+# la_scan_inputs and la_scan_grads of include/lightning.h.
+SCAN_INPUTS = struct.Struct("@5P5q3Pi4x")  # u delta z B C, their strides, A D delta_bias, softplus
+SCAN_GRADS = struct.Struct("@9P")  # du ddelta dz dB dC dA dD ddelta_bias dstate_in
 
 
 class LightningError(RuntimeError):
@@ -79,7 +71,7 @@ def lib():
         L.la_state_prefix.argtypes = [P, P, ctypes.POINTER(LL), I, I, I, I, I, P, P]
         L.la_output_norm_gate.argtypes = [P, P, P, ctypes.c_float, P, I, I, LL, I, I, I, P]
         L.la_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, LL, I, I, I, P, SZ, P]
-        SI, SG = ctypes.POINTER(ScanInputs), ctypes.POINTER(ScanGrads)
+        SI, SG = P, P  # packed structures
         L.la_selective_scan.argtypes = [P, I, SI, P, P, P, LL, I, I, I, I, I, P, SZ, P]
         L.la_selective_scan_step.argtypes = [SI, P, P, I, I, I, I, I, I, P]
         L.la_selective_scan_backward.argtypes = [P, I, SI, P, P, LL, P, SG, LL, I, I, I, I, I, P,
@@ -320,106 +312,109 @@ def backward(dout, q, k, v, slopes, out_dtype=None, stream=None):
 # cu_seqlens, [T, ...]; a token input may be a column slice of a wider tensor
 # (any stride between tokens, its last dimensions contiguous).
 
-def _rows(t, lead, inner, what):
-    """Pointer of a token tensor [*lead, *inner] and the elements between its tokens."""
-    if t.shape != lead + inner:
-        raise ValueError(f"{what} is {tuple(t.shape)}, expected {tuple(lead + inner)}")
-    dense = inner[0] if len(inner) == 1 else inner[0] * inner[1]
+def _rows(t, shape, lead, dense, what):
+    """Pointer of a token tensor and the elements between its tokens, of which
+    each has `dense` elements in the dimensions behind the `lead` first ones."""
+    if t.shape != shape:
+        raise ValueError(f"{what} is {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
-        return t.data_ptr() or None, dense
-    k, stride = len(lead), t.stride()
-    size = 1
-    for n, st in zip(reversed(inner), reversed(stride[k:])):
+        return t.data_ptr(), dense
+    stride, size = t.stride(), 1
+    for n, st in zip(reversed(shape[lead:]), reversed(stride[lead:])):
         if n != 1 and st != size:
             raise ValueError(f"{what}: the elements of a token must be contiguous")
         size *= n
-    if k == 2 and lead[1] > 1:
+    if lead == 2 and shape[1] > 1:
         ld = stride[1]
-        if lead[0] > 1 and stride[0] != lead[1] * ld:
+        if shape[0] > 1 and stride[0] != shape[1] * ld:
             raise ValueError(f"{what}: the tokens of all sequences must be evenly spaced")
     else:
-        ld = stride[0] if lead[0] > 1 else dense
-    return t.data_ptr() or None, ld
+        ld = stride[0] if shape[0] > 1 else dense
+    return t.data_ptr(), ld
 
 
 def _flat(t, shape, dtype, what):
-    """Pointer of a dense tensor of a given shape and dtype; None stays None."""
+    """Pointer of a dense tensor of a given shape and dtype; 0 for None."""
     if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype:
+        return 0
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr() if t.numel() else None
-
-
-def _same(first, *others):
-    """Every given tensor is on first's device, which is a GPU; its index."""
-    if not first.is_cuda:
-        raise ValueError(f"tensors must be on a GPU, not on {first.device}")
-    index = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors on {first.device} and on {t.device}")
-    return index
-
-
-def _sequences(x, cu_seqlens, features):
-    """(leading shape, number of sequences, rows, pointer of cu_seqlens)."""
-    if cu_seqlens is None:
-        if x.dim() != 2 + features:
-            raise ValueError(f"expected [B, N, ...] without cu_seqlens, got {tuple(x.shape)}")
-        lead = x.shape[:2]
-        return lead, lead[0], lead[0] * lead[1], None
-    if x.dim() != 1 + features:
-        raise ValueError(f"expected [T, ...] with cu_seqlens, got {tuple(x.shape)}")
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
-    lead = x.shape[:1]
-    return lead, cu_seqlens.numel() - 1, lead[0], _flat(cu_seqlens, cu_seqlens.shape, torch.int32,
-                                                        "cu_seqlens")
+    return t.data_ptr()
 
 
 _HERE_AND_NOW = contextlib.nullcontext()
 
 
-def _on(index, stream, inputs):
-    """(context, raw stream) of a call on GPU `index`: within the context the
-    device is current and allocations belong to the stream (default: the
-    device's current one). Inputs that a caller frees while the call runs on
-    another stream than theirs stay allocated until it is done."""
+def _on(stream, *tensors):
+    """(device index, context, raw stream) of a call on these tensors, None among
+    them, which are all on one GPU. Within the context that device is current
+    and allocations belong to the stream (default: the device's current one).
+    Inputs that a caller frees while the call runs on another stream than theirs
+    stay allocated until it is done."""
+    index = tensors[0].get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a GPU, not on {tensors[0].device}")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {tensors[0].device} and on {t.device}")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(index)
-        return (_HERE_AND_NOW if torch.cuda.current_device() == index
-                else torch.cuda.device(index)), raw
+        if torch.cuda.current_device() == index:
+            return index, _HERE_AND_NOW, raw
+        return index, torch.cuda.device(index), raw
     if stream.device.index != index:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     if stream != torch.cuda.current_stream(index):
-        for t in inputs:
+        for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    return torch.cuda.stream(stream), stream.cuda_stream  # makes its device current too
+    return index, torch.cuda.stream(stream), stream.cuda_stream  # makes its device current too
+
+
+def _sequences(x, cu_seqlens):
+    """(shape of the rows, number of sequences, rows, pointer of cu_seqlens)."""
+    shape = x.shape
+    if cu_seqlens is None:
+        if len(shape) != 3:
+            raise ValueError(f"expected [B, N, D] without cu_seqlens, got {tuple(shape)}")
+        return shape[:2], shape[0], shape[0] * shape[1], 0
+    if len(shape) != 2:
+        raise ValueError(f"expected [T, D] with cu_seqlens, got {tuple(shape)}")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [num_seqs + 1]")
+    return shape[:1], cu_seqlens.numel() - 1, shape[0], _flat(cu_seqlens, cu_seqlens.shape,
+                                                              torch.int32, "cu_seqlens")
+
+
+def _new(like, shape, dtype):
+    """An output like a token input, of another dtype where one is given."""
+    if (dtype is None or dtype == like.dtype) and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead):
-    """(la_scan_inputs, D, G, n) after checking every shape."""
-    width = u.shape[-1]
-    if A.dim() != 2 or B.dim() != len(lead) + 2:
-        raise ValueError(f"A is [D, n] and B [tokens, G, n], got {tuple(A.shape)}, {tuple(B.shape)}")
-    n, G = A.shape[1], B.shape[-2]
-    for t, what in ((delta, "delta"), (z, "z"), (B, "B"), (C, "C")):
-        if t is not None and t.dtype != u.dtype:
-            raise ValueError(f"{what} is {t.dtype}, u is {u.dtype}")
-    up, ld_u = _rows(u, lead, (width,), "u")
-    dp, ld_d = _rows(delta, lead, (width,), "delta")
-    bp, ld_b = _rows(B, lead, (G, n), "B")
-    cp, ld_c = _rows(C, lead, (G, n), "C")
-    zp, ld_z = (None, 0) if z is None else _rows(z, lead, (width,), "z")
-    f32 = torch.float32
-    s = ScanInputs(up, dp, zp, bp, cp, ld_u, ld_d, ld_z, ld_b, ld_c,
-                   _flat(A, (width, n), f32, "A"), _flat(D, (width,), f32, "D"),
-                   _flat(delta_bias, (width,), f32, "delta_bias"), 1 if softplus else 0)
-    return s, width, G, n
+    """(packed la_scan_inputs, D, G, n, in_t) after checking every shape."""
+    shape, ashape, dtype = u.shape, A.shape, u.dtype
+    if len(ashape) != 2 or B.dim() != lead + 2:
+        raise ValueError(f"A is [D, n] and B [tokens, G, n], got {tuple(ashape)}, {tuple(B.shape)}")
+    width, n, G = shape[-1], ashape[1], B.shape[-2]
+    if delta.dtype != dtype or B.dtype != dtype or C.dtype != dtype or (
+            z is not None and z.dtype != dtype):
+        raise ValueError(f"delta, z, B and C must be {dtype} as u is")
+    bc = (*shape[:-1], G, n)
+    up, ld_u = _rows(u, shape, lead, width, "u")
+    dp, ld_d = _rows(delta, shape, lead, width, "delta")
+    bp, ld_b = _rows(B, bc, lead, G * n, "B")
+    cp, ld_c = _rows(C, bc, lead, G * n, "C")
+    zp, ld_z = (0, 0) if z is None else _rows(z, shape, lead, width, "z")
+    f32, vector = torch.float32, (width,)
+    packed = SCAN_INPUTS.pack(up, dp, zp, bp, cp, ld_u, ld_d, ld_z, ld_b, ld_c,
+                              _flat(A, (width, n), f32, "A"), _flat(D, vector, f32, "D"),
+                              _flat(delta_bias, vector, f32, "delta_bias"), 1 if softplus else 0)
+    return packed, width, G, n, _dt(u)
 
 
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
@@ -427,20 +422,22 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     """Allocate outputs and workspace and run la_selective_scan. u, delta, z
     [B, N, D] (packed [T, D] with cu_seqlens), A [D, n], B and C [B, N, G, n],
     D and delta_bias [D], state_in [num_seqs, D, n]. Returns (y, state or None)."""
-    lead, seqs, rows, cu = _sequences(u, cu_seqlens, 1)
-    dev = _same(u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens)
-    s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead)
-    sp = _flat(state_in, (seqs, width, n), torch.float32, "state_in")
-    ctx, handle = _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens))
+    rows_shape, seqs, rows, cu = _sequences(u, cu_seqlens)
+    dev, ctx, handle = _on(stream, u, delta, A, B, C, D, z, delta_bias, state_in, cu_seqlens)
+    s, width, G, n, in_t = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus,
+                                        len(rows_shape))
+    states = (seqs, width, n)
+    sp = _flat(state_in, states, torch.float32, "state_in")
+    fn = lib()
     with ctx:
-        y = torch.empty((*lead, width), dtype=out_dtype or u.dtype, device=dev)
-        state = (torch.empty((seqs, width, n), dtype=torch.float32, device=dev)
-                 if want_state else None)
-        need = lib().la_workspace_bytes(LA_OP_SCAN, G, width, rows, n, seqs, _dt(u))
+        y = _new(u, u.shape, out_dtype)
+        state = torch.empty(states, dtype=torch.float32, device=dev) if want_state else None
+        need = fn.la_workspace_bytes(LA_OP_SCAN, G, width, rows, n, seqs, in_t)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check("la_selective_scan", lib().la_selective_scan(
-            cu, seqs, s, sp, y.data_ptr() or None, state.data_ptr() or None if want_state else None,
-            rows, width, G, n, _dt(u), _dt(y), ws.data_ptr() if need else None, need, handle))
+        status = fn.la_selective_scan(
+            cu, seqs, s, sp, y.data_ptr(), state.data_ptr() if want_state else 0, rows, width, G,
+            n, in_t, _dt(y), ws.data_ptr() if need else 0, need, handle)
+    _check("la_selective_scan", status)
     return y, state
 
 
@@ -450,15 +447,15 @@ def selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=Non
     [B, D], B and C [B, G, n]); state [B, D, n] is advanced in place. Returns y [B, D]."""
     if u.dim() != 2:
         raise ValueError(f"u is [B, D], got {tuple(u.shape)}")
-    dev = _same(u, delta, A, B, C, D, z, delta_bias, state)
-    s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, u.shape[:1])
+    _, ctx, handle = _on(stream, u, delta, A, B, C, D, z, delta_bias, state)
+    s, width, G, n, in_t = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, 1)
     seqs = u.shape[0]
     sp = _flat(state, (seqs, width, n), torch.float32, "state")
-    ctx, handle = _on(dev, stream, (u, delta, A, B, C, D, z, delta_bias, state))
     with ctx:
-        y = torch.empty((seqs, width), dtype=out_dtype or u.dtype, device=dev)
-        _check("la_selective_scan_step", lib().la_selective_scan_step(
-            s, sp, y.data_ptr() or None, seqs, width, G, n, _dt(u), _dt(y), handle))
+        y = _new(u, u.shape, out_dtype)
+        status = lib().la_selective_scan_step(s, sp, y.data_ptr(), seqs, width, G, n, in_t,
+                                              _dt(y), handle)
+    _check("la_selective_scan_step", status)
     return y
 
 
@@ -468,39 +465,40 @@ def selective_scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=No
     """Gradients of selective_scan for the output gradient dy (and dstate_out,
     that of the returned state). Returns a dict: du, ddelta, dB, dC, dA, and dz,
     dD, ddelta_bias, dstate_in where the call has that input."""
-    lead, seqs, rows, cu = _sequences(u, cu_seqlens, 1)
-    dev = _same(u, dy, delta, A, B, C, D, z, delta_bias, state_in, dstate_out, cu_seqlens)
-    s, width, G, n = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead)
+    rows_shape, seqs, rows, cu = _sequences(u, cu_seqlens)
+    dev, ctx, handle = _on(stream, u, dy, delta, A, B, C, D, z, delta_bias, state_in, dstate_out,
+                           cu_seqlens)
+    lead = len(rows_shape)
+    s, width, G, n, in_t = _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead)
     if dy.dtype != u.dtype:
         raise ValueError(f"dy is {dy.dtype}, u is {u.dtype}")
-    dyp, ld_dy = _rows(dy, lead, (width,), "dy")
-    f32 = torch.float32
-    sp = _flat(state_in, (seqs, width, n), f32, "state_in")
-    dsp = _flat(dstate_out, (seqs, width, n), f32, "dstate_out")
-    ctx, handle = _on(dev, stream, (dy, u, delta, A, B, C, D, z, delta_bias, state_in, dstate_out,
-                           cu_seqlens))
+    dyp, ld_dy = _rows(dy, u.shape, lead, width, "dy")
+    f32, states = torch.float32, (seqs, width, n)
+    sp = _flat(state_in, states, f32, "state_in")
+    dsp = _flat(dstate_out, states, f32, "dstate_out")
+    fn = lib()
     with ctx:
-        def new(shape, dtype=f32):
-            return torch.empty(shape, dtype=dtype, device=dev)
-
         t = out_dtype or u.dtype
-        out = {"du": new((*lead, width), t), "ddelta": new((*lead, width), t),
-               "dB": new((*lead, G, n), t), "dC": new((*lead, G, n), t), "dA": new((width, n))}
+        bc = (*rows_shape, G, n)
+        out = {"du": _new(u, u.shape, t), "ddelta": _new(u, u.shape, t),
+               "dB": torch.empty(bc, dtype=t, device=dev),
+               "dC": torch.empty(bc, dtype=t, device=dev), "dA": torch.empty_like(A)}
         if z is not None:
-            out["dz"] = new((*lead, width), t)
+            out["dz"] = _new(u, u.shape, t)
         if D is not None:
-            out["dD"] = new((width,))
+            out["dD"] = torch.empty_like(D)
         if delta_bias is not None:
-            out["ddelta_bias"] = new((width,))
+            out["ddelta_bias"] = torch.empty_like(delta_bias)
         if state_in is not None:
-            out["dstate_in"] = new((seqs, width, n))
-        g = ScanGrads(*[(out[f].data_ptr() or None) if f in out else None
-                        for f, _ in ScanGrads._fields_])
-        need = lib().la_workspace_bytes(LA_OP_SCAN_BACKWARD, G, width, rows, n, seqs, _dt(u))
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check("la_selective_scan_backward", lib().la_selective_scan_backward(
-            cu, seqs, s, sp, dyp, ld_dy, dsp, g, rows, width, G, n, _dt(u), _dt(out["du"]),
-            ws.data_ptr(), ws.numel(), handle))
+            out["dstate_in"] = torch.empty_like(state_in)
+        g = SCAN_GRADS.pack(*[out[f].data_ptr() if f in out else 0 for f in (
+            "du", "ddelta", "dz", "dB", "dC", "dA", "dD", "ddelta_bias", "dstate_in")])
+        need = fn.la_workspace_bytes(LA_OP_SCAN_BACKWARD, G, width, rows, n, seqs, in_t)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        status = fn.la_selective_scan_backward(
+            cu, seqs, s, sp, dyp, ld_dy, dsp, g, rows, width, G, n, in_t, _dt(out["du"]),
+            ws.data_ptr() if need else 0, need, handle)
+    _check("la_selective_scan_backward", status)
     return out
 
 
@@ -518,20 +516,19 @@ def short_conv(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, 
     """Allocate outputs and run la_short_conv. x [B, N, D] (packed [T, D] with
     cu_seqlens), weight [D, W], bias [D], state_in [num_seqs, W-1, D] of x's
     dtype. Returns (y, state or None)."""
-    lead, seqs, rows, cu = _sequences(x, cu_seqlens, 1)
-    dev = _same(x, weight, bias, state_in, cu_seqlens)
+    rows_shape, seqs, rows, cu = _sequences(x, cu_seqlens)
+    dev, ctx, handle = _on(stream, x, weight, bias, state_in, cu_seqlens)
     width, W, wp, bp = _conv_weights(x, weight, bias)
-    xp, ld_x = _rows(x, lead, (width,), "x")
-    sp = _flat(state_in, (seqs, W - 1, width), x.dtype, "state_in")
-    ctx, handle = _on(dev, stream, (x, weight, bias, state_in, cu_seqlens))
+    xp, ld_x = _rows(x, x.shape, len(rows_shape), width, "x")
+    states = (seqs, max(W - 1, 0), width)
+    sp = _flat(state_in, states, x.dtype, "state_in")
     with ctx:
-        y = torch.empty((*lead, width), dtype=out_dtype or x.dtype, device=dev)
-        state = (torch.empty((seqs, max(W - 1, 0), width), dtype=x.dtype, device=dev)
-                 if want_state else None)
-        _check("la_short_conv", lib().la_short_conv(
-            cu, seqs, xp, ld_x, wp, bp, sp, y.data_ptr() or None,
-            state.data_ptr() or None if want_state else None, rows, width, W, 1 if silu else 0,
-            _dt(x), _dt(y), handle))
+        y = _new(x, x.shape, out_dtype)
+        state = torch.empty(states, dtype=x.dtype, device=dev) if want_state else None
+        status = lib().la_short_conv(
+            cu, seqs, xp, ld_x, wp, bp, sp, y.data_ptr(), state.data_ptr() if want_state else 0,
+            rows, width, W, 1 if silu else 0, _dt(x), _dt(y), handle)
+    _check("la_short_conv", status)
     return y, state
 
 
@@ -540,17 +537,16 @@ def short_conv_step(x, weight, bias, state, silu=True, out_dtype=None, stream=No
     [B, W-1, D] is advanced in place. Returns y [B, D]."""
     if x.dim() != 2:
         raise ValueError(f"x is [B, D], got {tuple(x.shape)}")
-    dev = _same(x, weight, bias, state)
+    _, ctx, handle = _on(stream, x, weight, bias, state)
     width, W, wp, bp = _conv_weights(x, weight, bias)
     seqs = x.shape[0]
-    xp, ld_x = _rows(x, x.shape[:1], (width,), "x")
+    xp, ld_x = _rows(x, x.shape, 1, width, "x")
     sp = _flat(state, (seqs, W - 1, width), x.dtype, "state")
-    ctx, handle = _on(dev, stream, (x, weight, bias, state))
     with ctx:
-        y = torch.empty((seqs, width), dtype=out_dtype or x.dtype, device=dev)
-        _check("la_short_conv_step", lib().la_short_conv_step(
-            xp, ld_x, wp, bp, sp, y.data_ptr() or None, seqs, width, W, 1 if silu else 0, _dt(x),
-            _dt(y), handle))
+        y = _new(x, x.shape, out_dtype)
+        status = lib().la_short_conv_step(xp, ld_x, wp, bp, sp, y.data_ptr(), seqs, width, W,
+                                          1 if silu else 0, _dt(x), _dt(y), handle)
+    _check("la_short_conv_step", status)
     return y
 
 
@@ -558,34 +554,32 @@ def short_conv_backward(dy, x, weight, bias=None, silu=True, state_in=None, dsta
                         cu_seqlens=None, out_dtype=None, stream=None):
     """Gradients of short_conv. Returns a dict: dx, dweight, and dbias,
     dstate_in where the call has that input."""
-    lead, seqs, rows, cu = _sequences(x, cu_seqlens, 1)
-    dev = _same(x, dy, weight, bias, state_in, dstate_out, cu_seqlens)
+    rows_shape, seqs, rows, cu = _sequences(x, cu_seqlens)
+    dev, ctx, handle = _on(stream, x, dy, weight, bias, state_in, dstate_out, cu_seqlens)
     width, W, wp, bp = _conv_weights(x, weight, bias)
     if dy.dtype != x.dtype:
         raise ValueError(f"dy is {dy.dtype}, x is {x.dtype}")
-    xp, ld_x = _rows(x, lead, (width,), "x")
-    dyp, ld_dy = _rows(dy, lead, (width,), "dy")
-    sp = _flat(state_in, (seqs, W - 1, width), x.dtype, "state_in")
-    dsp = _flat(dstate_out, (seqs, W - 1, width), x.dtype, "dstate_out")
-    ctx, handle = _on(dev, stream, (dy, x, weight, bias, state_in, dstate_out, cu_seqlens))
+    xp, ld_x = _rows(x, x.shape, len(rows_shape), width, "x")
+    dyp, ld_dy = _rows(dy, x.shape, len(rows_shape), width, "dy")
+    states = (seqs, W - 1, width)
+    sp = _flat(state_in, states, x.dtype, "state_in")
+    dsp = _flat(dstate_out, states, x.dtype, "dstate_out")
+    fn, in_t = lib(), _dt(x)
     with ctx:
         t = out_dtype or x.dtype
-        out = {"dx": torch.empty((*lead, width), dtype=t, device=dev),
-               "dweight": torch.empty((width, W), dtype=torch.float32, device=dev)}
+        out = {"dx": _new(x, x.shape, t), "dweight": torch.empty_like(weight)}
         if bias is not None:
-            out["dbias"] = torch.empty((width,), dtype=torch.float32, device=dev)
+            out["dbias"] = torch.empty_like(bias)
         if state_in is not None:
-            out["dstate_in"] = torch.empty((seqs, W - 1, width), dtype=t, device=dev)
-
-        def ptr(f):
-            return (out[f].data_ptr() or None) if f in out else None
-
-        need = lib().la_workspace_bytes(LA_OP_CONV_BACKWARD, 1, width, rows, W, seqs, _dt(x))
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check("la_short_conv_backward", lib().la_short_conv_backward(
-            cu, seqs, dyp, ld_dy, xp, ld_x, wp, bp, sp, dsp, ptr("dx"), ptr("dweight"),
-            ptr("dbias"), ptr("dstate_in"), rows, width, W, 1 if silu else 0, _dt(x),
-            _dt(out["dx"]), ws.data_ptr(), ws.numel(), handle))
+            out["dstate_in"] = torch.empty(states, dtype=t, device=dev)
+        need = fn.la_workspace_bytes(LA_OP_CONV_BACKWARD, 1, width, rows, W, seqs, in_t)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        status = fn.la_short_conv_backward(
+            cu, seqs, dyp, ld_dy, xp, ld_x, wp, bp, sp, dsp, out["dx"].data_ptr(),
+            out["dweight"].data_ptr(), out["dbias"].data_ptr() if bias is not None else 0,
+            out["dstate_in"].data_ptr() if state_in is not None else 0, rows, width, W,
+            1 if silu else 0, in_t, _dt(out["dx"]), ws.data_ptr() if need else 0, need, handle)
+    _check("la_short_conv_backward", status)
     return out
 
 
@@ -593,42 +587,43 @@ def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, 
     """la_layer_norm over the last dimension of x (dense). Returns (y, mean,
     rstd); the last two, fp32 of x's leading shape, are what
     layer_norm_backward takes (None without want_stats)."""
-    dev = _same(x, weight, bias)
-    F = x.shape[-1]
-    xp = _flat(x, x.shape, x.dtype, "x")
-    wp = _flat(weight, (F,), torch.float32, "weight")
-    bp = _flat(bias, (F,), torch.float32, "bias")
+    dev, ctx, handle = _on(stream, x, weight, bias)
+    shape, f32 = x.shape, torch.float32
+    F = shape[-1]
+    xp = _flat(x, shape, x.dtype, "x")
+    wp, bp = _flat(weight, (F,), f32, "weight"), _flat(bias, (F,), f32, "bias")
     rows = x.numel() // F if F else 0
-    ctx, handle = _on(dev, stream, (x, weight, bias))
     with ctx:
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        y = _new(x, shape, out_dtype)
         mean = rstd = None
+        mp = rp = 0
         if want_stats:
-            mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
-        _check("la_layer_norm", lib().la_layer_norm(
-            xp, wp, bp, eps, y.data_ptr() or None, mean.data_ptr() or None if want_stats else None,
-            rstd.data_ptr() or None if want_stats else None, rows, F, _dt(x), _dt(y), handle))
+            mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+            rstd = torch.empty_like(mean)
+            mp, rp = mean.data_ptr(), rstd.data_ptr()
+        status = lib().la_layer_norm(xp, wp, bp, eps, y.data_ptr(), mp, rp, rows, F, _dt(x),
+                                     _dt(y), handle)
+    _check("la_layer_norm", status)
     return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, want_bias=True, out_dtype=None, stream=None):
     """Gradients of layer_norm: (dx, dweight, dbias); dbias is None without want_bias."""
-    dev = _same(x, dy, weight, mean, rstd)
-    F = x.shape[-1]
-    f32 = torch.float32
-    xp, dyp = _flat(x, x.shape, x.dtype, "x"), _flat(dy, x.shape, x.dtype, "dy")
+    dev, ctx, handle = _on(stream, x, dy, weight, mean, rstd)
+    shape, f32 = x.shape, torch.float32
+    F = shape[-1]
+    xp, dyp = _flat(x, shape, x.dtype, "x"), _flat(dy, shape, x.dtype, "dy")
     wp = _flat(weight, (F,), f32, "weight")
-    mp, rp = _flat(mean, x.shape[:-1], f32, "mean"), _flat(rstd, x.shape[:-1], f32, "rstd")
+    mp, rp = _flat(mean, shape[:-1], f32, "mean"), _flat(rstd, shape[:-1], f32, "rstd")
     rows = x.numel() // F if F else 0
-    ctx, handle = _on(dev, stream, (dy, x, weight, mean, rstd))
+    fn, in_t = lib(), _dt(x)
     with ctx:
-        dx = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
-        dw = torch.empty((F,), dtype=f32, device=dev)
-        db = torch.empty((F,), dtype=f32, device=dev) if want_bias else None
-        need = lib().la_workspace_bytes(LA_OP_NORM_BACKWARD, 1, F, rows, 1, 1, _dt(x))
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check("la_layer_norm_backward", lib().la_layer_norm_backward(
-            dyp, xp, wp, mp, rp, dx.data_ptr() or None, dw.data_ptr() or None,
-            db.data_ptr() or None if want_bias else None, rows, F, _dt(x), _dt(dx), ws.data_ptr(),
-            ws.numel(), handle))
+        dx, dw = _new(x, shape, out_dtype), torch.empty_like(weight)
+        db = torch.empty_like(weight) if want_bias else None
+        need = fn.la_workspace_bytes(LA_OP_NORM_BACKWARD, 1, F, rows, 1, 1, in_t)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        status = fn.la_layer_norm_backward(
+            dyp, xp, wp, mp, rp, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if want_bias else 0,
+            rows, F, in_t, _dt(dx), ws.data_ptr() if need else 0, need, handle)
+    _check("la_layer_norm_backward", status)
     return dx, dw, db

@@ -183,8 +183,8 @@ def test_scan_in_place_state_and_rows_behind_the_last_sequence():
     st = _rnd(torch.Generator().manual_seed(1), 2, D, n)
     d = {k: (v.contiguous().to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in p.items()}
     cu, T = _cu(lens), sum(lens) + 9
-    s = L.ScanInputs(*[d[k].data_ptr() for k in ("u", "delta", "z", "B", "C")], D, D, D, n, n,
-                     *[d[k].data_ptr() for k in ("A", "D", "delta_bias")], 1)
+    s = L.SCAN_INPUTS.pack(*[d[k].data_ptr() for k in ("u", "delta", "z", "B", "C")], D, D, D, n, n,
+                           *[d[k].data_ptr() for k in ("A", "D", "delta_bias")], 1)
     need = L.la_workspace_bytes(L.LA_OP_SCAN, 1, D, T, n, 2, F32)
     assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device=DEV)
@@ -198,7 +198,7 @@ def test_scan_in_place_state_and_rows_behind_the_last_sequence():
     R.check(y[:sum(lens)], want, by, "y")
     R.check(state, wst, bs, "state in place")
     assert (y[sum(lens):] == 7.0).all()
-    names = [f for f, _ in L.ScanGrads._fields_]
+    names = ["du", "ddelta", "dz", "dB", "dC", "dA", "dD", "ddelta_bias", "dstate_in"]
     shape = {"dB": (T, 1, n), "dC": (T, 1, n), "dA": (D, n), "dD": (D,), "ddelta_bias": (D,),
              "dstate_in": (2, D, n)}
     out = {f: torch.full(shape.get(f, (T, D)), 7.0, device=DEV) for f in names}
@@ -206,7 +206,7 @@ def test_scan_in_place_state_and_rows_behind_the_last_sequence():
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)  # NaN wherever it is read unwritten
     dy = torch.ones((T, D), device=DEV)
     assert L.lib().la_selective_scan_backward(
-        cu.data_ptr(), 2, s, None, dy.data_ptr(), D, None, L.ScanGrads(*[out[f].data_ptr() for f in names]),
+        cu.data_ptr(), 2, s, None, dy.data_ptr(), D, None, L.SCAN_GRADS.pack(*[out[f].data_ptr() for f in names]),
         T, D, 1, n, 1, 1, ws.data_ptr(), need, stream) == L.LA_OK
     one = torch.ones((sum(lens), D), dtype=torch.float64)
     spans = R.spans_of(lens)

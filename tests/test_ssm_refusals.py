@@ -22,9 +22,7 @@ def _inputs(**kw):
     a = dict(u=X, delta=X, z=X, B=X, C=X, ld_u=128, ld_delta=128, ld_z=128, ld_b=16, ld_c=16, A=X,
              D=X, delta_bias=X, softplus=1)
     a.update(kw)
-    return L.ScanInputs(*[a[f] or None if isinstance(a[f], int) and f in
-                          ("u", "delta", "z", "B", "C", "A", "D", "delta_bias") else a[f]
-                          for f, _ in L.ScanInputs._fields_])
+    return L.SCAN_INPUTS.pack(*a.values())
 
 
 def _scan(lib, cu=0, seqs=2, st=0, y=X, out=0, total=64, D=128, G=1, n=16, it=0, ot=0, ws=X,
@@ -87,7 +85,7 @@ def test_scan_step_refuses(lib, kw, status):
 def _scan_back(lib, dy=X, ld_dy=128, total=64, ws=X, wsb=1 << 40, grads=None, **kw):
     g = dict(du=X, ddelta=X, dz=X, dB=X, dC=X, dA=X, dD=X, ddelta_bias=X, dstate_in=X)
     g.update(grads or {})
-    out = L.ScanGrads(*[g[f] or None for f, _ in L.ScanGrads._fields_])
+    out = L.SCAN_GRADS.pack(*g.values())
     return lib.la_selective_scan_backward(None, 2, _inputs(**kw), None, P(dy) if dy else None, ld_dy,
                                           None, out, total, 128, 1, 16, 0, 0, P(ws) if ws else None,
                                           wsb, None)
@@ -184,13 +182,14 @@ def test_binding_refuses(lib):
         L.selective_scan(x[0], x[0], w, x, x)
     with pytest.raises(ValueError, match="int32"):
         L.short_conv(x[0], w, cu_seqlens=torch.zeros(3, dtype=torch.int64))
-    lead = torch.Size((2, 8))
-    assert L._rows(torch.zeros((2, 8, 128))[..., 64:], lead, (64,), "x")[1] == 128
-    assert L._rows(torch.zeros((2, 8, 100))[..., 4:36].unflatten(-1, (2, 16)), lead, (2, 16), "B")[1] == 100
-    assert L._rows(torch.zeros((1, 1, 64)), torch.Size((1, 1)), (64,), "x")[1] == 64
+    z = torch.zeros
+    assert L._rows(z((2, 8, 128))[..., 64:], (2, 8, 64), 2, 64, "x")[1] == 128
+    assert L._rows(z((2, 8, 100))[..., 4:36].unflatten(-1, (2, 16)), (2, 8, 2, 16), 2, 32, "B")[1] == 100
+    assert L._rows(z((1, 1, 64)), (1, 1, 64), 2, 64, "x")[1] == 64
+    assert L._rows(z((5, 128))[:, :64], (5, 64), 1, 64, "x")[1] == 128
     with pytest.raises(ValueError, match="contiguous"):
-        L._rows(torch.zeros((2, 8, 128))[..., ::2], lead, (64,), "x")
+        L._rows(z((2, 8, 128))[..., ::2], (2, 8, 64), 2, 64, "x")
     with pytest.raises(ValueError, match="evenly spaced"):
-        L._rows(torch.zeros((2, 16, 64))[:, :8], lead, (64,), "x")
+        L._rows(z((2, 16, 64))[:, :8], (2, 8, 64), 2, 64, "x")
     with pytest.raises(ValueError, match="expected"):
-        L._rows(torch.zeros((2, 8, 63)), lead, (64,), "x")
+        L._rows(z((2, 8, 63)), (2, 8, 64), 2, 64, "x")
