@@ -174,34 +174,44 @@ __global__ void __launch_bounds__(NT) conv_kernel(ConvArgs a)
         const int n = (int)((end < t1 ? end : t1) - t);  // rows of this run
         const T* xp = x + t * a.ld_x;
         To* yp = (To*)a.y + t * a.D + c;
+        auto row_out = [&](const Row<T, V>& in, int at) {
+            f2 out[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+                win[W - 1][i] = in.get(i);
+                f2 p = b[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
+                const f2 g = mul2(p, sigmoid2(p));
+                out[i] = a.silu ? g : p;
+            }
+            store_row<To, V>(yp + (long long)at * a.D, out);
+        };
+        // Whole groups of rows, so that the window's shifts are a renaming of
+        // registers; then the rest one by one.
+        const int whole = n / AHEAD * AHEAD;
         Row<T, V> rows[AHEAD];
         auto load = [&](int at) {
 #pragma unroll
-            for (int q = 0; q < AHEAD; ++q)
-                rows[q].load(xp + (long long)(at + q < n ? at + q : n - 1) * a.ld_x);
+            for (int q = 0; q < AHEAD; ++q) rows[q].load(xp + (long long)(at + q) * a.ld_x);
         };
-        load(0);
+        if (whole) load(0);
 #pragma unroll 1
-        for (int at = 0; at < n; at += AHEAD) {
+        for (int at = 0; at < whole; at += AHEAD) {
             Row<T, V> now[AHEAD];
 #pragma unroll
             for (int q = 0; q < AHEAD; ++q) now[q] = rows[q];
-            if (at + AHEAD < n) load(at + AHEAD);
+            if (at + AHEAD < whole) load(at + AHEAD);
 #pragma unroll
-            for (int q = 0; q < AHEAD; ++q) {
-                f2 out[H];
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-                    win[W - 1][i] = now[q].get(i);
-                    f2 p = b[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
-                    out[i] = a.silu ? mul2(p, sigmoid2(p)) : p;
-                }
-                if (at + q < n) store_row<To, V>(yp + (long long)(at + q) * a.D, out);
-            }
+            for (int q = 0; q < AHEAD; ++q) row_out(now[q], at + q);
+        }
+#pragma unroll 1
+        for (int at = whole; at < n; ++at) {
+            Row<T, V> in;
+            in.load(xp + (long long)at * a.ld_x);
+            row_out(in, at);
         }
         t += n;
     }
@@ -295,16 +305,14 @@ __global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
 #pragma unroll
             for (int j = W - 1; j > 0; --j) win[j][i] = win[j - 1][i], q[j][i] = q[j - 1][i];
             win[0][i] = oldest.get(i);
-            f2 g = grad.get(i);
-            if (a.silu) {
-                f2 p = b[i];
+            const f2 g = grad.get(i);
+            f2 p = b[i];
 #pragma unroll
-                for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
-                // y'(p) = sg (1 + p (1 - sg))
-                const f2 sg = sigmoid2(p);
-                g = mul2(g, mul2(sg, fma2(p, fma2(sg, minus, one), one)));
-            }
-            q[0][i] = g;
+            for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
+            // y'(p) = sg (1 + p (1 - sg))
+            const f2 sg = sigmoid2(p);
+            const f2 slope = mul2(sg, fma2(p, fma2(sg, minus, one), one));
+            q[0][i] = a.silu ? mul2(g, slope) : g;
         }
     };
     // Before row `last` of sequence s: no q after it, and its window but the oldest.
@@ -374,10 +382,10 @@ __global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
         const long long low = start > t0 ? start : t0;
         const int n = (int)(t - low + 1);
         To* out = (To*)a.dx + t * a.D + c;
-        auto finish = [&](long long tok, To* to) {
+        auto finish = [&](To* to, long long with_state) {
             f2 v[H];
             pull(v);
-            if (dst && tok >= end - (W - 1)) from_state(tok, v);
+            if (with_state >= 0) from_state(with_state, v);
             store_row<To, V>(to, v);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
@@ -386,9 +394,19 @@ __global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
                 db[i] = add2(db[i], q[0][i]);
             }
         };
-        // Whole groups of rows, so that the windows' shifts are a renaming of
-        // registers; then the rest one by one.
-        const int whole = n / BACK_AHEAD * BACK_AHEAD;
+        // The rows that state_out holds, one by one; whole groups of rows, so that
+        // the windows' shifts are a renaming of registers; the rest one by one.
+        const long long held = t - end + W;
+        const int head = dst && held > 0 ? (int)(held < n ? held : n) : 0;
+        const int whole = head + (n - head) / BACK_AHEAD * BACK_AHEAD;
+        auto single = [&](int at, bool with_state) {
+            Row<T, V> g;
+            g.load(dy + (t - at) * a.ld_dy);
+            step(input(t - at - (W - 1)), g);
+            finish(out - (long long)at * a.D, with_state ? t - at : -1);
+        };
+#pragma unroll 1
+        for (int at = 0; at < head; ++at) single(at, true);
         Row<T, V> xs[BACK_AHEAD], gs[BACK_AHEAD];
         auto load = [&](long long tok) {
             const T* xp = x + (tok - (W - 1)) * a.ld_x;
@@ -403,9 +421,9 @@ __global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
 #pragma unroll
             for (int k = 0; k < BACK_AHEAD; ++k) gs[k].load(gp - (long long)k * a.ld_dy);
         };
-        if (whole) load(t);
+        if (whole > head) load(t - head);
 #pragma unroll 1
-        for (int at = 0; at < whole; at += BACK_AHEAD) {
+        for (int at = head; at < whole; at += BACK_AHEAD) {
             Row<T, V> xn[BACK_AHEAD], gn[BACK_AHEAD];
 #pragma unroll
             for (int k = 0; k < BACK_AHEAD; ++k) xn[k] = xs[k], gn[k] = gs[k];
@@ -413,16 +431,11 @@ __global__ void __launch_bounds__(NT, 4) conv_backward_kernel(ConvArgs a)
 #pragma unroll
             for (int k = 0; k < BACK_AHEAD; ++k) {
                 step(xn[k], gn[k]);
-                finish(t - at - k, out - (long long)(at + k) * a.D);
+                finish(out - (long long)(at + k) * a.D, -1);
             }
         }
 #pragma unroll 1
-        for (int at = whole; at < n; ++at) {
-            Row<T, V> g;
-            g.load(dy + (t - at) * a.ld_dy);
-            step(input(t - at - (W - 1)), g);
-            finish(t - at, out - (long long)at * a.D);
-        }
+        for (int at = whole; at < n; ++at) single(at, false);
         t -= n;
     }
     float out[2 * H][W], ob[2 * H];
