@@ -181,6 +181,9 @@ def test_scan_in_place_state_and_rows_behind_the_last_sequence():
     lens, D, n = [200, 150], 20, 16
     p = _scan_problem(lens + [9], D, 1, n, F32, 11, sliced=False)
     st = _rnd(torch.Generator().manual_seed(1), 2, D, n)
+    for k in ("u", "delta", "z", "B", "C"):  # what is behind the last sequence is not read either
+        p[k] = p[k].clone()
+        p[k][sum(lens):] = float("nan")
     d = {k: (v.contiguous().to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in p.items()}
     cu, T = _cu(lens), sum(lens) + 9
     s = L.SCAN_INPUTS.pack(*[d[k].data_ptr() for k in ("u", "delta", "z", "B", "C")], D, D, D, n, n,
@@ -219,6 +222,48 @@ def test_scan_in_place_state_and_rows_behind_the_last_sequence():
             assert (out[f][sum(lens):] == 7.0).all(), f
 
 
+def test_scan_many_short_sequences():
+    """5000 packed sequences of 0 to 3 tokens, and one long one among them that is
+    cut into chunks: the table of chunks spans several rounds of its CTA."""
+    g = torch.Generator().manual_seed(0)
+    lens = torch.randint(0, 4, (5000,), generator=g).tolist()
+    lens[2500] = 500
+    D, n = 6, 4
+    p = _scan_problem(lens, D, 1, n, F32, 1)
+    st = _rnd(g, len(lens), D, n)
+    dy, ds = _rnd(g, sum(lens), D), _rnd(g, len(lens), D, n)
+    args, kw = _args(_to(p))
+    q = {k: _f64(v) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    spans = R.spans_of(lens)
+    y, out = L.selective_scan(*args, **kw, state_in=st.to(DEV), cu_seqlens=_cu(lens))
+    want, ws, by, bs, h = R.scan(q, spans, _f64(st))
+    R.check(y, want, by, "y")
+    R.check(out, ws, bs, "state")
+    got = L.selective_scan_backward(dy.to(DEV), *args, **kw, state_in=st.to(DEV), dstate_out=ds.to(DEV),
+                                    cu_seqlens=_cu(lens))
+    want = R.scan_backward(q, spans, h, _f64(dy), _f64(st), _f64(ds))
+    bounds = R.scan_backward_bounds(q, spans, _f64(dy), _f64(st), _f64(ds))
+    for k, v in got.items():
+        R.check(v, want[k], bounds[k], k)
+
+
+def test_scan_one_group_per_channel_and_strided_gradient():
+    """G = D, and dy as a slice of a wider tensor."""
+    lens, D, n = [40], 9, 5
+    p = _scan_problem(lens, D, D, n, BF, 13)
+    wide = _rnd(torch.Generator().manual_seed(1), 40, 30, dtype=BF)
+    args, kw = _args(_to(p))
+    q = {k: _f64(v) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    y, _ = L.selective_scan(*args, **kw, cu_seqlens=_cu(lens), out_dtype=F32)
+    want, _, by, _, h = R.scan(q, [(0, 40)])
+    R.check(y, want, by, "y")
+    got = L.selective_scan_backward(wide.to(DEV)[:, 3:12], *args, **kw, cu_seqlens=_cu(lens), out_dtype=F32)
+    dy = _f64(wide[:, 3:12])
+    want, bounds = R.scan_backward(q, [(0, 40)], h, dy), R.scan_backward_bounds(q, [(0, 40)], dy)
+    for k, v in got.items():
+        R.check(v, want[k], bounds[k], k)
+
+
 def test_scan_non_finite_inputs_stay_in_their_channel():
     lens, D, n = [90], 40, 16
     p = _scan_problem(lens, D, 1, n, F32, 12)
@@ -249,6 +294,12 @@ def test_scan_empty():
     g = L.selective_scan_backward(t(0, 8), t(0, 8), t(0, 8), t(8, 16), t(0, 1, 16), t(0, 1, 16),
                                   cu_seqlens=_cu([]))
     assert not g["dA"].any()
+    y, out = L.selective_scan(t(0, 7, 8), t(0, 7, 8), t(8, 16), t(0, 7, 1, 16), t(0, 7, 1, 16))
+    assert y.shape == (0, 7, 8) and out.shape == (0, 8, 16)
+    w = torch.ones((8, 4), device=DEV)
+    assert L.short_conv(t(0, 7, 8), w)[0].shape == (0, 7, 8)
+    assert not L.short_conv_backward(t(0, 7, 8), t(0, 7, 8), w)["dweight"].any()
+    assert L.short_conv_step(t(0, 8), w, None, t(0, 3, 8)).shape == (0, 8)
     assert L.selective_scan_step(t(0, 8), t(0, 8), t(8, 16), t(0, 1, 16), t(0, 1, 16), t(0, 8, 16)).shape == (0, 8)
 
 
@@ -374,6 +425,29 @@ def test_offsets_beyond_32_bits():
     n, mean, _ = L.layer_norm(x[0], b, b)
     assert torch.equal(n[-100:], L.layer_norm(x[0, -100:].contiguous(), b, b)[0])
     del n, x
+    torch.cuda.empty_cache()
+
+
+def test_scan_offsets_beyond_32_bits():
+    """2.3e9 elements per tensor: the last 64 rows are those of the same rows
+    continued from the state before them, to the bit (a whole number of tiles)."""
+    T, D, n = 70_016, 32_768, 16
+    g = torch.Generator(device=DEV).manual_seed(0)
+    u, dl = (torch.empty((1, T, D), dtype=BF, device=DEV) for _ in range(2))
+    for i in range(0, T, 4376):
+        u[0, i:i + 4376] = torch.randn((4376, D), generator=g, device=DEV)
+        dl[0, i:i + 4376] = torch.randn((4376, D), generator=g, device=DEV)
+    B, C = (torch.randn((1, T, 1, n), generator=g, device=DEV).to(BF) for _ in range(2))
+    A, b = -torch.rand((D, n), generator=g, device=DEV) * 4, torch.randn(D, device=DEV) - 3
+    y, st = L.selective_scan(u, dl, A, B, C, delta_bias=b)
+    cut = T - 64
+    last = y[:, cut:].clone()
+    del y
+    _, mid = L.selective_scan(u[:, :cut], dl[:, :cut], A, B[:, :cut], C[:, :cut], delta_bias=b)
+    torch.cuda.empty_cache()
+    y2, st2 = L.selective_scan(u[:, cut:], dl[:, cut:], A, B[:, cut:], C[:, cut:], delta_bias=b, state_in=mid)
+    assert torch.equal(y2, last) and torch.equal(st2, st)
+    del u, dl
     torch.cuda.empty_cache()
 
 

@@ -50,6 +50,7 @@ BAD_SCAN = [
     (dict(ld_u=127), L.LA_ERR_INVALID_ARG), (dict(ld_z=0), L.LA_ERR_INVALID_ARG),
     (dict(ld_b=15), L.LA_ERR_INVALID_ARG),
     (dict(total=(1 << 31) - 2), L.LA_ERR_UNSUPPORTED),
+    (dict(ld_u=(1 << 24) + 1), L.LA_ERR_UNSUPPORTED), (dict(ld_c=1 << 25), L.LA_ERR_UNSUPPORTED),
     (dict(seqs=1 << 25, total=0), L.LA_ERR_UNSUPPORTED),
     # a long prompt in a narrow layer is cut into chunks and needs a workspace
     (dict(total=1 << 16, ws=0), L.LA_ERR_WORKSPACE), (dict(total=1 << 16, wsb=64), L.LA_ERR_WORKSPACE),
@@ -93,6 +94,7 @@ def _scan_back(lib, dy=X, ld_dy=128, total=64, ws=X, wsb=1 << 40, grads=None, **
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dy=0), L.LA_ERR_INVALID_ARG), (dict(ld_dy=100), L.LA_ERR_INVALID_ARG),
+    (dict(ld_dy=1 << 25), L.LA_ERR_UNSUPPORTED),
     (dict(grads=dict(dA=0)), L.LA_ERR_INVALID_ARG), (dict(grads=dict(du=0)), L.LA_ERR_INVALID_ARG),
     (dict(grads=dict(dz=0)), L.LA_ERR_INVALID_ARG),   # a gate without its gradient
     (dict(z=0), L.LA_ERR_INVALID_ARG),                # and the reverse
