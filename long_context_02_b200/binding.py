@@ -392,7 +392,7 @@ def _new(like, shape, dtype):
     """An output like a token input, of another dtype where one is given."""
     if (dtype is None or dtype == like.dtype) and like.is_contiguous():
         return torch.empty_like(like)
-    return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def _scan_inputs(u, delta, A, B, C, D, z, delta_bias, softplus, lead):
@@ -431,7 +431,7 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=
     fn = lib()
     with ctx:
         y = _new(u, u.shape, out_dtype)
-        state = torch.empty(states, dtype=torch.float32, device=dev) if want_state else None
+        state = A.new_empty(states) if want_state else None
         need = fn.la_workspace_bytes(LA_OP_SCAN, G, width, rows, n, seqs, in_t)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         status = fn.la_selective_scan(
@@ -481,8 +481,7 @@ def selective_scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=No
         t = out_dtype or u.dtype
         bc = (*rows_shape, G, n)
         out = {"du": _new(u, u.shape, t), "ddelta": _new(u, u.shape, t),
-               "dB": torch.empty(bc, dtype=t, device=dev),
-               "dC": torch.empty(bc, dtype=t, device=dev), "dA": torch.empty_like(A)}
+               "dB": u.new_empty(bc, dtype=t), "dC": u.new_empty(bc, dtype=t), "dA": torch.empty_like(A)}
         if z is not None:
             out["dz"] = _new(u, u.shape, t)
         if D is not None:
@@ -517,14 +516,14 @@ def short_conv(x, weight, bias=None, silu=True, state_in=None, cu_seqlens=None, 
     cu_seqlens), weight [D, W], bias [D], state_in [num_seqs, W-1, D] of x's
     dtype. Returns (y, state or None)."""
     rows_shape, seqs, rows, cu = _sequences(x, cu_seqlens)
-    dev, ctx, handle = _on(stream, x, weight, bias, state_in, cu_seqlens)
+    _, ctx, handle = _on(stream, x, weight, bias, state_in, cu_seqlens)
     width, W, wp, bp = _conv_weights(x, weight, bias)
     xp, ld_x = _rows(x, x.shape, len(rows_shape), width, "x")
     states = (seqs, max(W - 1, 0), width)
     sp = _flat(state_in, states, x.dtype, "state_in")
     with ctx:
         y = _new(x, x.shape, out_dtype)
-        state = torch.empty(states, dtype=x.dtype, device=dev) if want_state else None
+        state = x.new_empty(states) if want_state else None
         status = lib().la_short_conv(
             cu, seqs, xp, ld_x, wp, bp, sp, y.data_ptr(), state.data_ptr() if want_state else 0,
             rows, width, W, 1 if silu else 0, _dt(x), _dt(y), handle)
@@ -571,7 +570,7 @@ def short_conv_backward(dy, x, weight, bias=None, silu=True, state_in=None, dsta
         if bias is not None:
             out["dbias"] = torch.empty_like(bias)
         if state_in is not None:
-            out["dstate_in"] = torch.empty(states, dtype=t, device=dev)
+            out["dstate_in"] = x.new_empty(states, dtype=t)
         need = fn.la_workspace_bytes(LA_OP_CONV_BACKWARD, 1, width, rows, W, seqs, in_t)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         status = fn.la_short_conv_backward(
@@ -587,7 +586,7 @@ def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, 
     """la_layer_norm over the last dimension of x (dense). Returns (y, mean,
     rstd); the last two, fp32 of x's leading shape, are what
     layer_norm_backward takes (None without want_stats)."""
-    dev, ctx, handle = _on(stream, x, weight, bias)
+    _, ctx, handle = _on(stream, x, weight, bias)
     shape, f32 = x.shape, torch.float32
     F = shape[-1]
     xp = _flat(x, shape, x.dtype, "x")
@@ -598,7 +597,7 @@ def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, 
         mean = rstd = None
         mp = rp = 0
         if want_stats:
-            mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+            mean = weight.new_empty(shape[:-1])
             rstd = torch.empty_like(mean)
             mp, rp = mean.data_ptr(), rstd.data_ptr()
         status = lib().la_layer_norm(xp, wp, bp, eps, y.data_ptr(), mp, rp, rows, F, _dt(x),
