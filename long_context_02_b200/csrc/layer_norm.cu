@@ -158,18 +158,22 @@ __device__ __forceinline__ void write_rows(const Share<T, TPR, V, CH>* xs, To* y
     }
 }
 
-// V elements at p as pairs.
-template <typename T, int V> __device__ __forceinline__ void load_pairs(f2* v, const T* p)
-{
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        if constexpr (sizeof(T) == 2)
-            v[i] = pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-        else v[i] = pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+// 16 bytes of a row as stored, V elements; read as pairs.
+template <typename T, int V> struct Raw {
+    uint4 q;
+    __device__ __forceinline__ void load(const T* p, bool ok)
+    {
+        q = make_uint4(0, 0, 0, 0);
+        if (ok) q = *reinterpret_cast<const uint4*>(p);
     }
-}
+    __device__ __forceinline__ f2 get(int i) const
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        if constexpr (sizeof(T) == 2)
+            return pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else return pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+};
 
 // 16 bytes to shared memory, asynchronously.
 __device__ __forceinline__ void copy16(void* to, const void* from)
@@ -320,23 +324,17 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1)
 #pragma unroll 1
     for (; row < rows; row += step, turn ^= 1) {
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        // This thread's pairs m of row r; zeros behind the row's end.
-        auto pairs = [&](int r, int m, f2* v) {
-            const int c = (tid + NT * m) * V;
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) v[i] = pack(0.f, 0.f);
-            if (c < F) load_pairs<T, V>(v, ring + (long long)(stage * R + r) * F + c);
-        };
+        Raw<T, V> xs[R][CH];  // zeros behind a row's end
         float mu[R], sq[R], mw[R], lo, hi;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             f2 s = pack(0.f, 0.f);
 #pragma unroll
             for (int m = 0; m < CH; ++m) {
-                f2 v[V / 2];
-                pairs(r, m, v);
+                const int c = (tid + NT * m) * V;
+                xs[r][m].load(ring + (long long)(stage * R + r) * F + c, c < F);
 #pragma unroll
-                for (int i = 0; i < V / 2; ++i) s = add2(s, v[i]);
+                for (int i = 0; i < V / 2; ++i) s = add2(s, xs[r][m].get(i));
             }
             unpack(s, lo, hi);
             mu[r] = lo + hi;
@@ -348,12 +346,10 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1)
             f2 s = pack(0.f, 0.f);
 #pragma unroll
             for (int m = 0; m < CH; ++m) {
-                f2 v[V / 2];
-                pairs(r, m, v);
                 if ((tid + NT * m) * V < F) {
 #pragma unroll
                     for (int i = 0; i < V / 2; ++i) {
-                        const f2 d = add2(v[i], pack(-mu[r], -mu[r]));
+                        const f2 d = add2(xs[r][m].get(i), pack(-mu[r], -mu[r]));
                         s = fma2(d, d, s);
                     }
                 }
@@ -391,12 +387,11 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1)
 #pragma unroll
             for (int m = 0; m < CH; ++m) {
                 const int c = (tid + NT * m) * V;
-                f2 v[V / 2];
                 float out[V];
-                pairs(r, m, v);
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
-                    const f2 d = mul2(add2(v[i], pack(-mu[r], -mu[r])), pack(sq[r], sq[r]));
+                    const f2 d =
+                        mul2(add2(xs[r][m].get(i), pack(-mu[r], -mu[r])), pack(sq[r], sq[r]));
                     const int h = m * V / 2 + i;
                     unpack(fma2(d, w[h], b[h]), out[2 * i], out[2 * i + 1]);
                 }
@@ -479,8 +474,12 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) norm_backward_ker
     for (; row < rows; row += step, turn ^= 1) {
         stats(row + step, mu_next, rs_next);
         if constexpr (RING) asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        // x and dy of row r, twice: for the sums, and again for dx.
-        auto load = [&](int r, f2* xv, f2* gv) {
+        // x and dy of a row as stored (without vectors: as pairs), zeros where there
+        // are none. Rows in shared memory are read twice, for the sums and for dx,
+        // rather than kept in registers.
+        Raw<T, V> xs[CH], gs[CH];
+        f2 x1[H] = {}, g1[H] = {};
+        auto load = [&](int r) {
             const bool ok = row + r < rows;
             const T *xr = x + (row + r) * F, *gr = dy + (row + r) * F;
             if constexpr (RING) {
@@ -491,39 +490,42 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) norm_backward_ker
 #pragma unroll
                 for (int m = 0; m < CH; ++m) {
                     const int c = (tid + NT * m) * V;
-#pragma unroll
-                    for (int i = 0; i < V / 2; ++i) xv[m * V / 2 + i] = gv[m * V / 2 + i] = zero;
-                    if (ok && c < F) {
-                        load_pairs<T, V>(xv + m * V / 2, xr + c);
-                        load_pairs<T, V>(gv + m * V / 2, gr + c);
-                    }
+                    xs[m].load(xr + c, ok && c < F);
+                    gs[m].load(gr + c, ok && c < F);
                 }
             } else {
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
                     const int c0 = column(h, 0), c1 = column(h, 1);
                     const bool k0 = ok && c0 < F, k1 = ok && c1 < F;
-                    xv[h] = pack(k0 ? to_f32(xr[c0]) : 0.f, k1 ? to_f32(xr[c1]) : 0.f);
-                    gv[h] = pack(k0 ? to_f32(gr[c0]) : 0.f, k1 ? to_f32(gr[c1]) : 0.f);
+                    x1[h] = pack(k0 ? to_f32(xr[c0]) : 0.f, k1 ? to_f32(xr[c1]) : 0.f);
+                    g1[h] = pack(k0 ? to_f32(gr[c0]) : 0.f, k1 ? to_f32(gr[c1]) : 0.f);
                 }
             }
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-                xv[h] = mul2(add2(xv[h], pack(-mu[r], -mu[r])), pack(rs[r], rs[r]));
         };
-        f2 xv[H], gv[H];
+        auto value = [&](int r, int h) {
+            f2 v;
+            if constexpr (VECTORS) v = xs[2 * h / V].get(h % (V / 2));
+            else v = x1[h];
+            return mul2(add2(v, pack(-mu[r], -mu[r])), pack(rs[r], rs[r]));
+        };
+        auto grad = [&](int h) {
+            if constexpr (VECTORS) return gs[2 * h / V].get(h % (V / 2));
+            else return g1[h];
+        };
         float m1[R], m2[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            load(r, xv, gv);
+            load(r);
             f2 s1 = zero, s2 = zero;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                dw[h] = fma2(gv[h], xv[h], dw[h]);
-                db[h] = add2(db[h], gv[h]);
-                const f2 e = mul2(gv[h], w[h]);
+                const f2 v = value(r, h), g = grad(h);
+                dw[h] = fma2(g, v, dw[h]);
+                db[h] = add2(db[h], g);
+                const f2 e = mul2(g, w[h]);
                 s1 = add2(s1, e);
-                s2 = fma2(e, xv[h], s2);
+                s2 = fma2(e, v, s2);
             }
             float a, b;
             unpack(s1, a, b);
@@ -551,13 +553,14 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) norm_backward_ker
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (R > 1 || RING) load(r, xv, gv);
+            if (RING || R > 1) load(r);
+            f2 dxv[H];
             const f2 minus_m1 = pack(-m1[r] / F, -m1[r] / F), minus_m2 = pack(-m2[r] / F, -m2[r] / F);
             const f2 scale = pack(rs[r], rs[r]);
             To* const out = dx + (row + r) * F;
 #pragma unroll
             for (int h = 0; h < H; ++h)
-                xv[h] = mul2(fma2(xv[h], minus_m2, fma2(gv[h], w[h], minus_m1)), scale);
+                dxv[h] = mul2(fma2(value(r, h), minus_m2, fma2(grad(h), w[h], minus_m1)), scale);
             if (row + r >= rows) continue;
             if constexpr (VECTORS) {
 #pragma unroll
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) norm_backward_ker
                     if (c < F) {
                         float v[V];
 #pragma unroll
-                        for (int i = 0; i < V; i += 2) unpack(xv[(m * V + i) / 2], v[i], v[i + 1]);
+                        for (int i = 0; i < V; i += 2) unpack(dxv[(m * V + i) / 2], v[i], v[i + 1]);
                         store_vec<To, V>(out + c, v);
                     }
                 }
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) norm_backward_ker
                 for (int h = 0; h < H; ++h) {
                     const int c0 = column(h, 0), c1 = column(h, 1);
                     float v0, v1;
-                    unpack(xv[h], v0, v1);
+                    unpack(dxv[h], v0, v1);
                     if (c0 < F) out[c0] = from_f32<To>(v0);
                     if (c1 < F) out[c1] = from_f32<To>(v1);
                 }
@@ -665,7 +668,7 @@ cudaError_t launch_ring(const void* x, const float* weight, const float* bias, f
     } while (0)
 #define LA_NORM_TYPES(SIZES)                                                                     \
     if (in_t == LA_F32) { if (F % 4 == 0) SIZES(float, float, 4); else SIZES(float, float, 1); } \
-    else if (out_t == LA_F32) {                                                                  \
+    else if (dxvt == LA_F32) {                                                                  \
         if (F % 8 == 0) SIZES(__nv_bfloat16, float, 8); else SIZES(__nv_bfloat16, float, 1);     \
     } else {                                                                                     \
         if (F % 8 == 0) SIZES(__nv_bfloat16, __nv_bfloat16, 8);                                  \
@@ -674,7 +677,7 @@ cudaError_t launch_ring(const void* x, const float* weight, const float* bias, f
 
 cudaError_t launch_layer_norm(const void* x, const float* weight, const float* bias, float eps,
                               void* y, float* mean, float* rstd, long long rows, int F, int in_t,
-                              int out_t, cudaStream_t stream)
+                              int dxvt, cudaStream_t stream)
 {
 #define LA_WARP(T, To, V, CH)                                                                    \
     norm_warp_kernel<T, To, V, CH><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(              \
@@ -731,7 +734,7 @@ cudaError_t launch_backward(const void* dy, const void* x, const float* weight, 
 cudaError_t launch_layer_norm_backward(const void* dy, const void* x, const float* weight,
                                        const float* mean, const float* rstd, void* dx,
                                        float* dweight, float* dbias, long long rows, int F,
-                                       int in_t, int out_t, void* ws, cudaStream_t stream)
+                                       int in_t, int dxvt, void* ws, cudaStream_t stream)
 {
     const int ctas = back_ctas(rows, F);
     float* dw = (float*)ws;
