@@ -1,14 +1,18 @@
 // Layer norm forward and backward (formulas in lightning.h).
 //
-// Streams bound by HBM. A row is held in registers by TPR threads (a warp for
-// short rows, so that no barrier is needed), at most PER elements each, loaded
-// once: the mean, then the centred sum of squares, then the output come from
-// the registers. Rows are read in 16-byte vectors when F allows, else element
-// by element.
+// Streams bound by HBM. Rows are read once, in 16-byte vectors when F allows,
+// else element by element; the mean, the centred squares and the output come
+// from registers or shared memory. Up to 1024 features (2048 for few rows) a
+// warp holds a row, so that no barrier is needed; beyond, a CTA does. Many rows
+// are walked by CTAs that stay, several rows at a time, with the weights in
+// registers (they are fp32, twice as wide as bf16 rows) and the next rows on
+// their way into shared memory: a grid of one CTA per row took 230-310 us where
+// this takes 185 (32K rows of 8192, bf16, 5.8 TB/s).
 //
 // Backward: the row's two means give dx; dweight and dbias are sums down the
 // columns, which a CTA gathers in registers over the rows it walks and writes
-// as one partial row each; a second launch adds the partial rows.
+// as one partial row each; a second launch adds the partial rows. 16K rows of
+// 8192, bf16: 154 us, 5.2 TB/s.
 #include "ssm_scan.cuh"
 
 namespace la {

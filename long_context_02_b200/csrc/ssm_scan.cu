@@ -5,8 +5,13 @@
 //
 // A channel's n states are scanned token by token in registers: the chain
 // from token to token is one multiply-add, everything else is off it. What
-// bounds it is the exponentials: n per (token, channel) plus four for the
-// softplus and the gate, at 16 per clock and SM.
+// bounds it is the special function unit, 16 results per clock and SM: n
+// exponentials per (token, channel), and two each for the softplus and the
+// gate. For n = 16 that is 4.3 ps per (token, channel) on 148 SMs at 1.965 GHz,
+// against 1.2 ps for the bf16 inputs and outputs at 6.5 TB/s. Measured: 8 x 2K
+// tokens of 8192 channels 797 us, 5.9 ps; 8K tokens of one sequence 505 us, 7.5
+// ps (64 channels per CTA leave 20 SMs idle and one scanning warp to each
+// scheduler of the others).
 //
 // When the channels of all sequences do not fill the GPU, the sequences are
 // cut into chunks: a first launch computes every chunk's state from zero (the
@@ -14,7 +19,8 @@
 // exponential exp(A sum dt) is the chunk's whole decay; the second launch
 // folds the chunks before its own, h <- exp(A sum dt_c) h + h_c, and scans
 // with outputs. That takes the exponentials twice, so it pays from about
-// three chunks on.
+// three chunks on: 46K packed fp32 tokens of 1024 channels take 664 us, 287 in
+// the first launch and 387 in the second.
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -359,6 +365,8 @@ __device__ __forceinline__ void serve_threads(const ScanArgs& a, const Place& p,
 // what a thread reads from shared memory per token (B, C and its dt, dt u, a
 // wavefront per word whether other lanes read the same word or not) otherwise
 // takes longer than its exponentials: with one channel, 8K x 8192 took 681 us.
+// 512 servers where every CTA has an SM to itself (505 us against 572 with 256),
+// 256 where two CTAs share one (8 x 2K x 8192: 797 us against 943 with one).
 template <typename T, int K, int MODE, bool VEC, int SV>
 __global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanArgs a)
 {
@@ -387,7 +395,9 @@ __global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanAr
 // sequences, for which it reads the weights once and whose loads it starts
 // together. What depends on the channel alone is shared out: each of the
 // channel's K lanes makes dt, dt u and the gate of BB / K sequences, passes the
-// former on, and finishes the output of the same ones.
+// former on, and finishes the output of the same ones. 256 sequences of 8192
+// channels, 16 states: 61 us, 4.7 TB/s (every lane making every element 120 us,
+// with bounds checks on whole vectors 95 us).
 constexpr int BB = 4;
 
 // Four of B or C at p (the thread's first is m0 of n).
@@ -541,7 +551,8 @@ struct ForwardPlan {
     int items;
 };
 
-// How the forward scan is cut. A packed batch's lengths are not known here, so
+// How the forward scan is cut: into about two CTAs per SM (three or four per SM
+// took 817 and 671 us against 668 on the packed batch above). A packed batch's lengths are not known here, so
 // that it counts as one long sequence: where its sequences are shorter than a
 // chunk, the first launch finds nothing to do.
 ForwardPlan plan_forward(bool packed, int G, int D, long long total, int n, int num_seqs)

@@ -19,6 +19,13 @@
 // As in the forward scan a thread holds four states of two channels: what it
 // reads from shared memory per token, and the sums over channels (shuffles take
 // the same path), would otherwise take longer than the exponentials.
+//
+// 2 x 4K tokens of 4096 channels, 16 states, bf16: 1,102 us (bytes alone 72 us;
+// the exponentials of three walks and the elementwise ones 400 us), of which
+// the local pass 250, combine 30, the main pass 780, the sums 40. No single unit
+// bounds the main pass: its warps issue in 57% of the cycles, the special
+// function unit is busy in 39%, shared memory in 45%, and four CTAs per SM
+// instead of three gain nothing. One channel per thread took 2,104 us in all.
 #include <climits>
 
 #include "ssm_scan.cuh"
