@@ -7,14 +7,14 @@
 namespace la {
 namespace {
 
-constexpr int NT = 1024;
+constexpr int NT = 256;
 
 // Threads that share the rows of a column (a power of two): enough of them that
-// the CTAs, NT / strands columns each, fill the GPU twice.
+// there are 1024 threads per SM.
 int strands_for(int rows, long long cols)
 {
     int s = 1;
-    while (s < 32 && 2 * s <= rows && cols * s < 2LL * 148 * NT) s *= 2;
+    while (s < 32 && 2 * s <= rows && cols * s < 148LL * 1024) s *= 2;
     return s;
 }
 
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(NT) column_sums_kernel(SumJobs jobs)
     }
     float v = 0.f;
     if (c < cols) {
-#pragma unroll 8
+#pragma unroll 16
         for (int r = y; r < job.rows; r += job.strands) v += job.in[r * job.cols + c];
     }
     if (job.strands > 1) {

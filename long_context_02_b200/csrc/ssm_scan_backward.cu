@@ -313,36 +313,29 @@ __global__ void __launch_bounds__(128) combine_kernel(BackArgs a, const float* s
     const int first = a.ch.first_of(s), end = a.ch.end_of(s);
     float h = state_in ? state_in[s * DN + e] : 0.f;
     float g = dstate_out ? dstate_out[s * DN + e] : 0.f;
-    // Reads of AHEAD chunks at a time, before the writes to the same places.
+    // Both sweeps together, AHEAD chunks of each at a time: reads first, then the
+    // writes to the same places.
     constexpr int AHEAD = 8;
-    float local[AHEAD], decay[AHEAD];
-    for (int i = first; i < end; i += AHEAD) {
+    float hl[AHEAD], hd[AHEAD], gl[AHEAD], gd[AHEAD];
+    const int chunks = end - first;
+    for (int i = 0; i < chunks; i += AHEAD) {
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const long long at = i + k < end ? i + k : end - 1;
-            local[k] = a.hs[at * DN + e];
-            decay[k] = a.dtsum[at * a.D + c];
+            const int at = min(i + k, chunks - 1);
+            const long long up = first + at, down = end - 1 - at;
+            hl[k] = a.hs[up * DN + e];
+            hd[k] = a.dtsum[up * a.D + c];
+            gl[k] = a.gs[down * DN + e];
+            gd[k] = a.dtsum[down * a.D + c];
         }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (i + k < end) {
-                a.hs[(i + k) * DN + e] = h;
-                h = fmaf(ex2(A2 * decay[k]), h, local[k]);
-            }
-    }
-    for (int i = end - 1; i >= first; i -= AHEAD) {
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-            const long long at = i - k >= first ? i - k : first;
-            local[k] = a.gs[at * DN + e];
-            decay[k] = a.dtsum[at * a.D + c];
+            if (i + k >= chunks) break;
+            a.hs[(first + i + k) * DN + e] = h;
+            h = fmaf(ex2(A2 * hd[k]), h, hl[k]);
+            a.gs[(end - 1 - i - k) * DN + e] = g;
+            g = fmaf(ex2(A2 * gd[k]), g, gl[k]);
         }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (i - k >= first) {
-                a.gs[(i - k) * DN + e] = g;
-                g = fmaf(ex2(A2 * decay[k]), g, local[k]);
-            }
     }
     if (a.out.dstate_in) a.out.dstate_in[s * DN + e] = g;
 }
