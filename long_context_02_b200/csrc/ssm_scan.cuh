@@ -114,15 +114,31 @@ __device__ __forceinline__ f2 atanh_ratio(f2 q)
     p = fma2(p, q, pack(0.33333156f, 0.33333156f));
     return fma2(p, q, pack(1.f, 1.f));
 }
-__device__ __forceinline__ f2 softplus2(f2 v)
+__device__ __forceinline__ f2 log1p_part(f2 e)
 {
-    float x, y, a, b;
-    unpack(v, x, y);
-    const f2 e = exp_neg_abs2(x, y);
+    float a, b;
     unpack(add2(e, pack(2.f, 2.f)), a, b);
     const f2 s = mul2(e, pack(rcp(a), rcp(b)));
-    return fma2(mul2(s, pack(2.f, 2.f)), atanh_ratio(mul2(s, s)),
-                pack(relu_nan(x), relu_nan(y)));
+    return mul2(mul2(s, pack(2.f, 2.f)), atanh_ratio(mul2(s, s)));
+}
+__device__ __forceinline__ f2 softplus2(f2 v)
+{
+    float x, y;
+    unpack(v, x, y);
+    return add2(log1p_part(exp_neg_abs2(x, y)), pack(relu_nan(x), relu_nan(y)));
+}
+// With its derivative.
+__device__ __forceinline__ f2 softplus2(f2 v, f2& slope)
+{
+    float x, y, e0, e1, a, b;
+    unpack(v, x, y);
+    const f2 e = exp_neg_abs2(x, y);
+    unpack(e, e0, e1);
+    unpack(add2(e, pack(1.f, 1.f)), a, b);
+    // x < 0: e / (1 + e); NaN: itself
+    slope = mul2(pack(rcp(a), rcp(b)), pack(x >= 0.f ? 1.f : x < 0.f ? e0 : x,
+                                            y >= 0.f ? 1.f : y < 0.f ? e1 : y));
+    return add2(log1p_part(e), pack(relu_nan(x), relu_nan(y)));
 }
 __device__ __forceinline__ float softplus_f(float x)
 {
@@ -136,19 +152,6 @@ __device__ __forceinline__ f2 sigmoid2(f2 x)
     unpack(add2(ex2_2(mul2(x, pack(-SCAN_LOG2E, -SCAN_LOG2E))), pack(1.f, 1.f)), a, b);
     return pack(rcp(a), rcp(b));
 }
-// The derivative of softplus.
-__device__ __forceinline__ f2 softplus_slope2(f2 v)
-{
-    float x, y, e0, e1, a, b;
-    unpack(v, x, y);
-    const f2 e = exp_neg_abs2(x, y);
-    unpack(e, e0, e1);
-    unpack(add2(e, pack(1.f, 1.f)), a, b);
-    // x < 0: e / (1 + e); NaN: itself
-    return mul2(pack(rcp(a), rcp(b)), pack(x >= 0.f ? 1.f : x < 0.f ? e0 : x,
-                                           y >= 0.f ? 1.f : y < 0.f ? e1 : y));
-}
-
 // Sum V values over the M lanes that differ in the bits [STEP, STEP M) of the
 // lane number. Each step halves the values that a lane keeps, so V values
 // cost about V shuffles instead of V log2 M. On return lane l holds, in v[0

@@ -154,9 +154,16 @@ template <int K> struct Block {
     float c[BLK][NP];
 };
 
+// What the main pass's elementwise end needs of a block, made with the rest.
+template <int K> struct Slopes {
+    f2 dt[BLK][NT / K];  // d dt / d delta
+    f2 z[BLK][NT / K];   // dy times the gate's derivative
+};
+
 template <typename T, int K, bool VEC>
 __device__ __forceinline__ void fill_block(Block<K>& blk, const Inputs<T, K, VEC>& in, int n,
-                                           int rmax, f2 bias, bool softplus)
+                                           int rmax, f2 bias, bool softplus,
+                                           Slopes<K>* slopes = nullptr)
 {
     using I = Inputs<T, K, VEC>;
     const int pr = threadIdx.x % I::CP, bm = threadIdx.x % I::NP;
@@ -165,11 +172,21 @@ __device__ __forceinline__ void fill_block(Block<K>& blk, const Inputs<T, K, VEC
         const int row = in.prow + e * I::RP;
         if (BLK % I::RP && row >= BLK) continue;
         f2 dt = add2(in.d[e].get(), bias), w = in.y[e].get();
-        if (softplus) dt = softplus2(dt);
+        if (slopes) {
+            f2 slope = pack(1.f, 1.f);
+            if (softplus) dt = softplus2(dt, slope);
+            slopes->dt[row][pr] = slope;
+        } else if (softplus) {
+            dt = softplus2(dt);
+        }
         f2 du = mul2(dt, in.u[e].get());
         if (in.gated) {
-            const f2 z = in.z[e].get();
-            w = mul2(w, mul2(z, sigmoid2(z)));
+            const f2 z = in.z[e].get(), sg = sigmoid2(z), gate = mul2(z, sg);
+            // (z sg)' = sg + z sg (1 - sg)
+            if (slopes)
+                slopes->z[row][pr] =
+                    mul2(w, fma2(gate, fma2(sg, pack(-1.f, -1.f), pack(1.f, 1.f)), sg));
+            w = mul2(w, gate);
         }
         if (row > rmax || !in.lo_ok) dt = du = w = pack(0.f, 0.f);  // decay 1, nothing added
         if (!in.hi_ok) {  // a channel of the next group adds nothing to this one's sums
@@ -347,28 +364,26 @@ template <int K> struct MainShared {
     // C . h, for both channels.
     f2 gB[BLK][NT], gA[BLK][NT], y[BLK][NT];
     float red[NT / 32][BLK][2][NP];  // dB and dC, summed over each warp's channels
+    Slopes<K> slopes;
 };
 
-template <typename T, int K, bool VEC>
-__device__ __forceinline__ void store_two(const BackArgs& a, void* p, long long row, int c, bool hi,
-                                          f2 v)
+// A pair of outputs at p.
+template <bool VEC>
+__device__ __forceinline__ void store_two(char* p, bool f32, bool hi, f2 v)
 {
     float x, y;
     unpack(v, x, y);
-    const long long at = row * a.D + c;
-    if (a.out_f32) {
-        float* o = (float*)p + at;
-        if (VEC) *reinterpret_cast<f2*>(o) = v;
+    if (f32) {
+        if (VEC) *reinterpret_cast<f2*>(p) = v;
         else {
-            o[0] = x;
-            if (hi) o[1] = y;
+            reinterpret_cast<float*>(p)[0] = x;
+            if (hi) reinterpret_cast<float*>(p)[1] = y;
         }
     } else {
-        __nv_bfloat16* o = (__nv_bfloat16*)p + at;
-        if (VEC) *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(x, y);
+        if (VEC) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
         else {
-            o[0] = __float2bfloat16_rn(x);
-            if (hi) o[1] = __float2bfloat16_rn(y);
+            reinterpret_cast<__nv_bfloat16*>(p)[0] = __float2bfloat16_rn(x);
+            if (hi) reinterpret_cast<__nv_bfloat16*>(p)[1] = __float2bfloat16_rn(y);
         }
     }
 }
@@ -417,17 +432,28 @@ __global__ void __launch_bounds__(NT, 3) main_kernel(BackArgs a)
     I in(a, p);
     const f2 bias = channel_pair(a.in.delta_bias, ec, p.c_end);
     const f2 Dw = channel_pair(a.in.D, ec, p.c_end);
-    const f2 zero = pack(0.f, 0.f), one = pack(1.f, 1.f), minus = pack(-1.f, -1.f);
+    const f2 zero = pack(0.f, 0.f);
     f2 dD = zero, db = zero;
+    // Where the chunk's outputs start, and this thread's offset in bytes.
+    const int os = a.out_f32 ? 4 : 2;
+    const long long out0 = (p.t0 * a.D + p.c0) * os;
+    const uint32_t out_at = (uint32_t)(in.prow * a.D + 2 * epr) * os;
+    // dB and dC: this thread's state and tensor, and its first token of a block.
+    static_assert(2 * NP <= NT, "a token's values fit the threads");
+    constexpr int RT = NT / (2 * NP);  // tokens per round
+    const int bm = tid % NP, bwhich = tid / NP % 2, bq = tid / (2 * NP);
+    const long long per_token = (long long)a.G * a.n;
+    float* const bc_out = (bwhich ? a.dCp : a.dBp) +
+                          ((long long)p.cbg * a.view.total + p.t0) * per_token + (long long)p.g * a.n + bm;
     const int len = (int)(p.t1 - p.t0), nblk = (len + BLK - 1) / BLK;
     if (nblk > 0) in.load(nblk - 1, len - (nblk - 1) * BLK - 1);
 #pragma unroll 1
     for (int b = nblk - 1; b >= 0; --b) {
         const int rmax = min(BLK, len - b * BLK) - 1;
-        fill_block<T, K, VEC>(sh.in, in, a.n, rmax, bias, a.in.softplus);
-        Pair<T, VEC> cu[I::E], cd[I::E], cz[I::E], cy[I::E];
+        fill_block<T, K, VEC>(sh.in, in, a.n, rmax, bias, a.in.softplus, &sh.slopes);
+        Pair<T, VEC> cu[I::E];
 #pragma unroll
-        for (int e = 0; e < I::E; ++e) cu[e] = in.u[e], cd[e] = in.d[e], cz[e] = in.z[e], cy[e] = in.y[e];
+        for (int e = 0; e < I::E; ++e) cu[e] = in.u[e];
         __syncthreads();
         if (b > 0) in.load(b - 1, BLK - 1);
 
@@ -548,37 +574,34 @@ __global__ void __launch_bounds__(NT, 3) main_kernel(BackArgs a)
         for (int e = 0; e < I::E; ++e) {
             const int row = in.prow + e * I::RP;
             if (row > rmax || !in.lo_ok) continue;
-            const long long tok = p.t0 + b * BLK + row;
-            const f2 u = cu[e].get(), gb = sum_shares<K>(&sh.gB[row][epr * K]);
+            const f2 u = cu[e].get(), w = sh.in.w[row][epr];
+            const f2 gb = sum_shares<K>(&sh.gB[row][epr * K]);
             const f2 ga = sum_shares<K>(&sh.gA[row][epr * K]);
-            f2 w = cy[e].get();
-            if (in.gated) {
-                const f2 z = cz[e].get(), sg = sigmoid2(z), gate = mul2(z, sg);
-                const f2 y = fma2(Dw, u, sum_shares<K>(&sh.y[row][epr * K]));
-                // (z sg)' = sg + z sg (1 - sg)
-                const f2 slope = fma2(gate, fma2(sg, minus, one), sg);
-                store_two<T, K, VEC>(a, a.out.dz, tok, ec, in.hi_ok, mul2(mul2(w, y), slope));
-                w = mul2(w, gate);
-            }
             const float4 dtv = sh.in.dt[row][epr];
             const f2 dt = pack(dtv.x, dtv.z);
-            store_two<T, K, VEC>(a, a.out.du, tok, ec, in.hi_ok, fma2(Dw, w, mul2(dt, gb)));
-            f2 dd = fma2(ga, pack(SCAN_LN2, SCAN_LN2), mul2(u, gb));
-            if (a.in.softplus) dd = mul2(dd, softplus_slope2(add2(cd[e].get(), bias)));
-            store_two<T, K, VEC>(a, a.out.ddelta, tok, ec, in.hi_ok, dd);
+            const f2 dd = mul2(fma2(ga, pack(SCAN_LN2, SCAN_LN2), mul2(u, gb)),
+                               sh.slopes.dt[row][epr]);
+            // The rows' part of the address is the same for all threads.
+            const long long at = out0 + (long long)(b * BLK + e * I::RP) * a.D * os;
+            if (in.gated) {
+                const f2 y = fma2(Dw, u, sum_shares<K>(&sh.y[row][epr * K]));
+                store_two<VEC>((char*)a.out.dz + at + out_at, a.out_f32, in.hi_ok,
+                               mul2(sh.slopes.z[row][epr], y));
+            }
+            store_two<VEC>((char*)a.out.du + at + out_at, a.out_f32, in.hi_ok,
+                           fma2(Dw, w, mul2(dt, gb)));
+            store_two<VEC>((char*)a.out.ddelta + at + out_at, a.out_f32, in.hi_ok, dd);
             dD = fma2(w, u, dD);
             db = add2(db, dd);
         }
-        for (int i = tid; i < 2 * BLK * NP; i += NT) {
-            const int m = i % NP, which = i / NP % 2, q = i / (2 * NP);
+#pragma unroll
+        for (int r = 0; r < BLK; r += RT) {
+            const int q = r + bq;
+            if (q > rmax || bm >= a.n) continue;
             float v = 0.f;
 #pragma unroll
-            for (int k = 0; k < NT / 32; ++k) v += sh.red[k][q][which][m];
-            if (m < a.n && q <= rmax) {
-                float* to = which ? a.dCp : a.dBp;
-                const long long tok = p.t0 + b * BLK + q;
-                to[(((long long)p.cbg * a.view.total + tok) * a.G + p.g) * a.n + m] = v;
-            }
+            for (int k = 0; k < NT / 32; ++k) v += sh.red[k][q][bwhich][bm];
+            bc_out[(b * BLK + q) * per_token] = v;
         }
         __syncthreads();
     }
