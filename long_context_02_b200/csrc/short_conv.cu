@@ -10,7 +10,7 @@
 // its incoming state.
 //
 // Measured, bf16, W = 4: 4 x 8K tokens of 8192 channels 191-200 us, 5.4-5.6 TB/s.
-// The backward of 2 x 8K takes 205 us, 3.9 TB/s: its arithmetic (about 27
+// The backward of 2 x 8K takes 202 us, 4.0 TB/s: its arithmetic (about 27
 // instructions per element and thread, two of them on the special function
 // unit) sets the pace, not memory; two channels per thread, for more warps per
 // SM, took 250 us.

@@ -20,12 +20,13 @@
 // reads from shared memory per token, and the sums over channels (shuffles take
 // the same path), would otherwise take longer than the exponentials.
 //
-// 2 x 4K tokens of 4096 channels, 16 states, bf16: 1,102 us (bytes alone 72 us;
+// 2 x 4K tokens of 4096 channels, 16 states, bf16: 1,038 us (bytes alone 72 us;
 // the exponentials of three walks and the elementwise ones 400 us), of which
-// the local pass 250, combine 30, the main pass 780, the sums 40. No single unit
-// bounds the main pass: its warps issue in 57% of the cycles, the special
-// function unit is busy in 39%, shared memory in 45%, and four CTAs per SM
-// instead of three gain nothing. One channel per thread took 2,104 us in all.
+// the local pass 250, combine 25, the main pass 735, the sums 30. No single unit
+// bounds the main pass: its warps issue in 55% of the cycles, the special
+// function unit is busy in 39%, shared memory in half of them, and four CTAs per
+// SM instead of three gain nothing; fewer instructions do. One channel per
+// thread took 2,104 us in all.
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -154,7 +155,9 @@ template <int K> struct Block {
     float c[BLK][NP];
 };
 
-// What the main pass's elementwise end needs of a block, made with the rest.
+// What the main pass's elementwise end needs of a block, made with the rest: the
+// exponentials are at hand there, and 1,080 us became 1,038 (with the outputs'
+// addresses taken per row).
 template <int K> struct Slopes {
     f2 dt[BLK][NT / K];  // d dt / d delta
     f2 z[BLK][NT / K];   // dy times the gate's derivative
