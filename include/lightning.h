@@ -301,8 +301,8 @@ LA_API int la_backward(const void* dO, const void* q, const void* k, const void*
  * - in_t is the dtype of the token inputs, out_t that of the token outputs
  *   (the same combinations as elsewhere); weights, states of the scan and
  *   sums over tokens are fp32.
- * - total <= LA_MAX_TOKENS, num_seqs * D <= 2^31 - 1 and every ld of more than
- *   one token is at most LA_MAX_LD (LA_ERR_UNSUPPORTED above).
+ * - total <= LA_MAX_TOKENS, num_seqs * D <= 2^30, and D and every ld of more
+ *   than one token are at most LA_MAX_LD (LA_ERR_UNSUPPORTED above).
  * - Outputs must not overlap inputs, except where stated. The current device
  *   must be the tensors'.
  */

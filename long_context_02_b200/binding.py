@@ -588,6 +588,8 @@ def layer_norm(x, weight, bias=None, eps=1e-5, want_stats=True, out_dtype=None, 
     layer_norm_backward takes (None without want_stats)."""
     _, ctx, handle = _on(stream, x, weight, bias)
     shape, f32 = x.shape, torch.float32
+    if not shape:
+        raise ValueError("x has no dimension to normalise over")
     F = shape[-1]
     xp = _flat(x, shape, x.dtype, "x")
     wp, bp = _flat(weight, (F,), f32, "weight"), _flat(bias, (F,), f32, "bias")
@@ -610,6 +612,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_bias=True, out_dtype=Non
     """Gradients of layer_norm: (dx, dweight, dbias); dbias is None without want_bias."""
     dev, ctx, handle = _on(stream, x, dy, weight, mean, rstd)
     shape, f32 = x.shape, torch.float32
+    if not shape:
+        raise ValueError("x has no dimension to normalise over")
     F = shape[-1]
     xp, dyp = _flat(x, shape, x.dtype, "x"), _flat(dy, shape, x.dtype, "dy")
     wp = _flat(weight, (F,), f32, "weight")

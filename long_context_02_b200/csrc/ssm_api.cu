@@ -1,19 +1,31 @@
 // C ABI of the state space layer: argument checks and dispatch. The public
 // contract of every entry point is documented in include/lightning.h.
-#include <climits>
 #include <cstdint>
 
 #include "ssm.h"
 
 namespace la {
 
+namespace {
+
+// Features and states that keep every index of a row, every count of chunks and
+// every grid within 31 bits.
+bool sizes_fit(int D, int num_seqs)
+{
+    return D <= LA_MAX_LD && (long long)num_seqs * D <= (1 << 30);
+}
+
+}  // namespace
+
 size_t ssm_workspace_bytes(int op, int G, int D, long long total, int n, int num_seqs)
 {
-    if (D <= 0 || total < 0 || total > LA_MAX_TOKENS) return 0;
+    if (D <= 0 || total < 0 || total > LA_MAX_TOKENS || D > LA_MAX_LD) return 0;
     switch (op) {
     case LA_OP_SCAN:
     case LA_OP_SCAN_BACKWARD:
-        if (G <= 0 || D % G || n <= 0 || n > LA_MAX_SCAN_STATES || num_seqs < 0) return 0;
+        if (G <= 0 || D % G || n <= 0 || n > LA_MAX_SCAN_STATES || num_seqs < 0 ||
+            !sizes_fit(D, num_seqs))
+            return 0;
         return scan_workspace(op == LA_OP_SCAN_BACKWARD, G, D, total, n, num_seqs);
     case LA_OP_CONV_BACKWARD:
         if (n < 2 || n > 4) return 0;
@@ -44,7 +56,7 @@ int check_sequences(const int* cu, int num_seqs, long long total, int D, SeqView
     if (num_seqs < 0 || total < 0 || D <= 0) return LA_ERR_INVALID_ARG;
     if (num_seqs == 0 && total > 0) return LA_ERR_INVALID_ARG;  // rows of no sequence
     if (!cu && num_seqs > 0 && total % num_seqs) return LA_ERR_INVALID_ARG;
-    if (total > LA_MAX_TOKENS || (long long)num_seqs * D > INT_MAX) return LA_ERR_UNSUPPORTED;
+    if (total > LA_MAX_TOKENS || !sizes_fit(D, num_seqs)) return LA_ERR_UNSUPPORTED;
     if (!aligned(cu, 4)) return LA_ERR_INVALID_ARG;
     v.cu = cu;
     v.num_seqs = num_seqs;

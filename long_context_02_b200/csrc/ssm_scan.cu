@@ -501,34 +501,34 @@ __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float
 __global__ void __launch_bounds__(1024) plan_chunks_kernel(SeqView v, long long len, int items,
                                                            int* first, int* seq_of)
 {
-    __shared__ int warp_sum[32];
+    __shared__ long long warp_sum[32];  // offsets that are not sorted can pass 32 bits
     __shared__ int carry;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     if (tid == 0) carry = 0;
     __syncthreads();
     for (int base = 0; base < v.num_seqs; base += 1024) {
         const int s = base + tid;
-        int x = 0;
+        long long x = 0;
         if (s < v.num_seqs) {
             long long t0, t1;
             v.range(s, t0, t1);
             const long long c = (t1 - t0 + len - 1) / len;
-            x = (int)(c > 1 ? c : 1);
+            x = c > 1 ? c : 1;
         }
-        int sum = x;
+        long long sum = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, o);
+            const long long up = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += up;
         }
         if (lane == 31) warp_sum[w] = sum;
         __syncthreads();
-        int before = carry;
+        long long before = carry;
         for (int i = 0; i < w; ++i) before += warp_sum[i];
-        int at = before + sum - x;  // offsets that are not sorted could pass the table's end
-        if (s < v.num_seqs) first[s] = at < items ? at : items;
+        const long long at = before + sum - x;  // nor may they pass the table's end
+        if (s < v.num_seqs) first[s] = (int)(at < items ? at : items);
         __syncthreads();
-        if (tid == 1023) carry = before + sum < items ? before + sum : items;
+        if (tid == 1023) carry = (int)(before + sum < items ? before + sum : items);
         __syncthreads();
     }
     if (tid == 0) first[v.num_seqs] = carry;

@@ -195,3 +195,33 @@ def test_binding_refuses(lib):
         L._rows(z((2, 16, 64))[:, :8], (2, 8, 64), 2, 64, "x")
     with pytest.raises(ValueError, match="expected"):
         L._rows(z((2, 8, 63)), (2, 8, 64), 2, 64, "x")
+
+
+def test_sizes_beyond_31_bits_are_refused(lib):
+    """More features than LA_MAX_LD, or more than 2^30 states, in calls that no stride refuses."""
+    wide, many = (1 << 24) + 128, (1 << 30) + 2
+    x = P(X)
+    assert _scan(lib, total=1, seqs=1, D=wide) == L.LA_ERR_UNSUPPORTED
+    assert _scan(lib, total=0, seqs=many, D=1, n=1) == L.LA_ERR_UNSUPPORTED
+    assert _step(lib, B=1, D=wide) == L.LA_ERR_UNSUPPORTED
+    assert _step(lib, B=many, D=1, ld_u=1, ld_delta=1, ld_z=1, n=1, ld_b=1, ld_c=1) == L.LA_ERR_UNSUPPORTED
+    grads = L.SCAN_GRADS.pack(*[X] * 9)
+    assert lib.la_selective_scan_backward(None, 1, _inputs(), None, x, wide, None, grads, 1, wide, 1,
+                                          16, 0, 0, x, 1 << 60, None) == L.LA_ERR_UNSUPPORTED
+    assert _conv(lib, total=1, seqs=1, D=(1 << 31) - 1) == L.LA_ERR_UNSUPPORTED
+    assert _conv(lib, total=0, seqs=many, D=1, ld=1) == L.LA_ERR_UNSUPPORTED
+    assert lib.la_short_conv_step(x, wide, x, x, x, x, 1, wide, 4, 1, 0, 0, None) == L.LA_ERR_UNSUPPORTED
+    size = L.la_workspace_bytes
+    assert size(L.LA_OP_SCAN_BACKWARD, 1, wide, 1, 16, 1) == 0
+    assert size(L.LA_OP_SCAN_BACKWARD, 1, 1, 0, 1, many) == 0
+    assert size(L.LA_OP_SCAN, 1, 1, 1 << 20, 1, many) == 0
+    assert size(L.LA_OP_CONV_BACKWARD, 1, (1 << 31) - 1, 1, 4, 1) == 0
+
+
+def test_binding_refuses_norm_of_a_scalar(lib, monkeypatch):
+    monkeypatch.setattr(L, "_on", lambda *a: (0, None, 0))
+    one = torch.zeros(())
+    with pytest.raises(ValueError, match="no dimension"):
+        L.layer_norm(one, torch.zeros(1))
+    with pytest.raises(ValueError, match="no dimension"):
+        L.layer_norm_backward(one, one, torch.zeros(1), one, one)
