@@ -27,6 +27,7 @@
 // function unit is busy in 39%, shared memory in half of them, and four CTAs per
 // SM instead of three gain nothing; fewer instructions do. One channel per
 // thread took 2,104 us in all.
+#include <cfloat>
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -194,6 +195,8 @@ __device__ __forceinline__ void fill_block(Block<K>& blk, const Inputs<T, K, VEC
         if (row > rmax || !in.lo_ok) dt = du = w = pack(0.f, 0.f);  // decay 1, nothing added
         if (!in.hi_ok) {  // a channel of the next group adds nothing to this one's sums
             float lo, hi;
+            unpack(dt, lo, hi);
+            dt = pack(lo, 0.f);
             unpack(du, lo, hi);
             du = pack(lo, 0.f);
             unpack(w, lo, hi);
@@ -228,6 +231,11 @@ __device__ __forceinline__ void load_decays(f2 (*A)[2], const BackArgs& a, int c
     for (int x = 0; x < 2; ++x) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (c + x < c_end) load_states(v, a.in.A + (long long)(c + x) * a.n, m0, a.n);
+        // States behind n: the decay is 1 but for an infinite dt, where it is 0 as
+        // elsewhere; with A = 0 it would be NaN, and with it the channel's sums.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (m0 + i >= a.n) v[i] = -FLT_MIN;
         A[x][0] = pack(v[0] * SCAN_LOG2E, v[1] * SCAN_LOG2E);
         A[x][1] = pack(v[2] * SCAN_LOG2E, v[3] * SCAN_LOG2E);
     }

@@ -281,6 +281,31 @@ def test_scan_non_finite_inputs_stay_in_their_channel():
     R.check(y[:20, 7], want[:20, 7], by[:20, 7], "tokens before the infinity")
 
 
+@pytest.mark.parametrize("D,n", [(41, 10), (40, 10), (41, 16), (40, 3)])
+def test_scan_backward_of_an_infinite_step(D, n):
+    """An infinite dt forgets the state, so that the tokens before it get the
+    finite gradients of a sequence that ends there, in its channel too, and
+    dB stays finite everywhere else. The sums that remain are a part of those
+    without the infinity, whose bounds therefore hold."""
+    lens, at, ch = [90], 60, D - 1
+    p = _scan_problem(lens, D, 1, n, F32, 21)
+    q = {k: _f64(v) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    spans = R.spans_of(lens)
+    dy = _rnd(torch.Generator().manual_seed(22), sum(lens), D)
+    bounds = R.scan_backward_bounds(q, spans, _f64(dy))
+    p["delta"][at, ch] = q["delta"][at, ch] = float("inf")
+    want = R.scan_backward(q, spans, R.scan(q, spans)[4], _f64(dy))
+    args, kw = _args(_to(p))
+    got = L.selective_scan_backward(dy.to(DEV), *args, **kw, cu_seqlens=_cu(lens))
+    for k in ("du", "ddelta", "dz", "dB", "dC"):
+        assert torch.isfinite(want[k][:at]).all()
+        R.check(got[k][:at], want[k][:at], bounds[k][:at], k)
+    R.check(got["dB"][at + 1:], want["dB"][at + 1:], bounds["dB"][at + 1:], "dB behind it")
+    for k in ("du", "ddelta", "dz"):
+        R.check(got[k][:, :ch], want[k][:, :ch], bounds[k][:, :ch], f"{k} of the others")
+    R.check(got["dA"][:ch], want["dA"][:ch], bounds["dA"][:ch], "dA of the others")
+
+
 def test_scan_empty():
     t = lambda *s: torch.zeros(s, device=DEV)  # noqa: E731
     st = torch.randn((3, 8, 16), device=DEV)
