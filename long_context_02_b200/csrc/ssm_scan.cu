@@ -88,7 +88,7 @@ __device__ __forceinline__ void scan_threads(const ScanArgs& a, const Place& p, 
         if (c >= p.c_end) continue;
         load_states(A[x], a.in.A + (long long)c * a.n, m0, a.n);
 #pragma unroll
-        for (int i = 0; i < S; ++i) A[x][i] *= SCAN_LOG2E;
+        for (int i = 0; i < S; ++i) A[x][i] = decay_rate(A[x][i]);
         const float* in = a.state_in ? a.state_in + ((long long)p.s * a.D + c) * a.n : nullptr;
         const long long slot = ((long long)p.item * a.D + c) * a.n;
         if (MODE == 1) {
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(la_scan_inputs in, float
     }
     load_states<FULL>(A, in.A + (long long)c * n, m0, n);
 #pragma unroll
-    for (int s = 0; s < S; ++s) A[s] *= SCAN_LOG2E;
+    for (int s = 0; s < S; ++s) A[s] = decay_rate(A[s]);
     const float bias = in.delta_bias ? in.delta_bias[c] : 0.f;
     float acc[BB];
 #pragma unroll

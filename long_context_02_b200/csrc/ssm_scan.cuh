@@ -8,6 +8,8 @@
 // and coalesced, and passed through shared memory.
 #pragma once
 
+#include <cfloat>
+
 #include "ssm.h"
 
 namespace la {
@@ -28,6 +30,15 @@ __device__ __forceinline__ float rcp(float x)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// A log2 e, the decay's rate per dt. An infinite A (a state that forgets at once)
+// is the lowest number, so that the dt of 0 that stands for a row behind a
+// sequence's end is a decay of 1 there too.
+__device__ __forceinline__ float decay_rate(float A)
+{
+    const float r = A * SCAN_LOG2E;
+    return r < -FLT_MAX ? -FLT_MAX : r;
 }
 
 // Pairs of fp32 in one 64-bit register, for the packed instructions: one issue

@@ -27,7 +27,6 @@
 // function unit is busy in 39%, shared memory in half of them, and four CTAs per
 // SM instead of three gain nothing; fewer instructions do. One channel per
 // thread took 2,104 us in all.
-#include <cfloat>
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -236,8 +235,8 @@ __device__ __forceinline__ void load_decays(f2 (*A)[2], const BackArgs& a, int c
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (m0 + i >= a.n) v[i] = -FLT_MIN;
-        A[x][0] = pack(v[0] * SCAN_LOG2E, v[1] * SCAN_LOG2E);
-        A[x][1] = pack(v[2] * SCAN_LOG2E, v[3] * SCAN_LOG2E);
+        A[x][0] = pack(decay_rate(v[0]), decay_rate(v[1]));
+        A[x][1] = pack(decay_rate(v[2]), decay_rate(v[3]));
     }
 }
 __device__ __forceinline__ void load_pair(f2 (*v)[2], const float* p, const BackArgs& a,
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(128) combine_kernel(BackArgs a, const float* s
     const long long e = (long long)(blockIdx.x % per) * 128 + threadIdx.x;
     if (e >= DN) return;
     const int c = (int)(e / a.n);
-    const float A2 = a.in.A[e] * SCAN_LOG2E;
+    const float A2 = decay_rate(a.in.A[e]);
     const int first = a.ch.first_of(s), end = a.ch.end_of(s);
     float h = state_in ? state_in[s * DN + e] : 0.f;
     float g = dstate_out ? dstate_out[s * DN + e] : 0.f;

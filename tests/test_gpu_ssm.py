@@ -306,6 +306,35 @@ def test_scan_backward_of_an_infinite_step(D, n):
     R.check(got["dA"][:ch], want["dA"][:ch], bounds["dA"][:ch], "dA of the others")
 
 
+def test_scan_forgets_at_once_where_a_is_infinite():
+    """A state with A = -inf is dt u B of its own token; the gradients that its
+    formula leaves finite (all but ddelta of its channel) agree, packed with an
+    empty sequence and lengths that end inside a block. The bounds are those of
+    A = -40: they grow with sums of absolute values, whose terms a decay above 0
+    only adds to."""
+    lens, D, n, ch, m = [45, 0, 13], 24, 16, 5, 2
+    p = _scan_problem(lens, D, 1, n, F32, 23)
+    q = {k: _f64(v) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+    g = torch.Generator().manual_seed(24)
+    st, dy = _rnd(g, 3, D, n), _rnd(g, sum(lens), D)
+    spans = R.spans_of(lens)
+    q["A"][ch, m] = -40.0
+    _, _, by, bs, _ = R.scan(q, spans, _f64(st))
+    bounds = R.scan_backward_bounds(q, spans, _f64(dy), _f64(st))
+    p["A"][ch, m] = q["A"][ch, m] = float("-inf")
+    want, ws, _, _, h = R.scan(q, spans, _f64(st))
+    args, kw = _args(_to(p))
+    y, out = L.selective_scan(*args, **kw, state_in=st.to(DEV), cu_seqlens=_cu(lens))
+    R.check(y, want, by, "y")
+    R.check(out, ws, bs, "state")
+    grads = R.scan_backward(q, spans, h, _f64(dy), _f64(st))
+    got = L.selective_scan_backward(dy.to(DEV), *args, **kw, state_in=st.to(DEV), cu_seqlens=_cu(lens))
+    rest = torch.arange(D) != ch
+    for k in ("du", "dz", "dB", "dC", "dA", "dstate_in"):
+        R.check(got[k], grads[k], bounds[k], k)
+    R.check(got["ddelta"][:, rest.to(DEV)], grads["ddelta"][:, rest], bounds["ddelta"][:, rest], "ddelta")
+
+
 def test_scan_empty():
     t = lambda *s: torch.zeros(s, device=DEV)  # noqa: E731
     st = torch.randn((3, 8, 16), device=DEV)
