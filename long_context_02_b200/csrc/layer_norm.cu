@@ -7,12 +7,12 @@
 // are walked by CTAs that stay, several rows at a time, with the weights in
 // registers (they are fp32, twice as wide as bf16 rows) and the next rows on
 // their way into shared memory: a grid of one CTA per row took 230-310 us where
-// this takes 185 (32K rows of 8192, bf16, 5.8 TB/s).
+// this takes 185-203 (32K rows of 8192, bf16, 5.3-5.8 TB/s).
 //
 // Backward: the row's two means give dx; dweight and dbias are sums down the
 // columns, which a CTA gathers in registers over the rows it walks and writes
 // as one partial row each; a second launch adds the partial rows. 16K rows of
-// 8192, bf16: 154 us, 5.2 TB/s.
+// 8192, bf16: 154-168 us, 4.8-5.2 TB/s.
 #include "ssm_scan.cuh"
 
 namespace la {

@@ -9,8 +9,8 @@
 // regard to sequences: at a sequence's first token the window is reloaded from
 // its incoming state.
 //
-// Measured, bf16, W = 4: 4 x 8K tokens of 8192 channels 191-200 us, 5.4-5.6 TB/s.
-// The backward of 2 x 8K takes 202 us, 4.0 TB/s: its arithmetic (about 27
+// Measured, bf16, W = 4: 4 x 8K tokens of 8192 channels 191-203 us, 5.3-5.6 TB/s.
+// The backward of 2 x 8K takes 202-206 us, 3.9-4.0 TB/s: its arithmetic (about 27
 // instructions per element and thread, two of them on the special function
 // unit) sets the pace, not memory; two channels per thread, for more warps per
 // SM, took 250 us.
