@@ -18,7 +18,8 @@
  * ---------------------------------------
  * - All tensor pointers are DEVICE pointers owned by the caller, 16-byte
  *   aligned, dense and row-major. The library never allocates device memory;
- *   scratch space is the caller's `workspace`.
+ *   scratch space is the caller's `workspace`. (The state space layer asks for
+ *   less: see there.)
  * - Shapes: q, k, v, o are [B][H][N][d] (head dim d = d_k = d_v); packed
  *   variable-length inputs are [H][total][d]; states are [B][H][d][d] fp32.
  * - `slopes` is a device fp32 array [H] (s_h, finite, >= 0: not checked,
@@ -297,7 +298,11 @@ LA_API int la_backward(const void* dO, const void* q, const void* k, const void*
  * - A tensor that comes with an `ld` has `ld` elements between consecutive
  *   tokens (ld >= its features; elements of one token are contiguous) and
  *   needs the alignment of its elements only, so it can be a column slice of
- *   a wider projection. Every other tensor is dense and 16-byte aligned.
+ *   a wider projection. Every other tensor is dense; its address is a multiple
+ *   of the largest power of two, at most 16, that divides the bytes of one of its
+ *   slices along the first dimension (of the whole tensor for A, weight, their
+ *   gradients and vectors). So slices x[i:] of a 16-byte aligned tensor, and the
+ *   tensors of a stack of them, can be passed. The workspace is 16-byte aligned.
  * - in_t is the dtype of the token inputs, out_t that of the token outputs
  *   (the same combinations as elsewhere); weights, states of the scan and
  *   sums over tokens are fp32.

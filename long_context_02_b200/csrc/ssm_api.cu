@@ -40,7 +40,15 @@ size_t ssm_workspace_bytes(int op, int G, int D, long long total, int n, int num
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-bool aligned16(const void* p) { return aligned(p, 16); }
+// Of a dense tensor whose slices along the first dimension have `count` elements of
+// `size` bytes (weights: the whole tensor): aligned to the largest power of two, at
+// most 16, that divides them. The kernels choose vectors by widths alone, so a width
+// that allows none asks for no more than its elements' alignment.
+bool dense(const void* p, long long count, size_t size)
+{
+    const size_t bytes = (size_t)count * size, most = bytes & (~bytes + 1);
+    return aligned(p, most < 16 ? most : 16);
+}
 size_t elem(int t) { return t == LA_BF16 ? 2 : 4; }
 
 int check_types(int in_t, int out_t)
@@ -74,7 +82,8 @@ int check_scan(const la_scan_inputs* in, long long rows, int D, int G, int n, in
         return LA_ERR_INVALID_ARG;
     const size_t e = elem(in_t);
     if (!aligned(in->u, e) || !aligned(in->delta, e) || !aligned(in->z, e) || !aligned(in->B, e) ||
-        !aligned(in->C, e) || !aligned16(in->A) || !aligned16(in->D) || !aligned16(in->delta_bias))
+        !aligned(in->C, e) || !dense(in->A, (long long)D * n, 4) || !dense(in->D, D, 4) ||
+        !dense(in->delta_bias, D, 4))
         return LA_ERR_INVALID_ARG;
     const long long bc = (long long)G * n;
     if (rows > 1 && (in->ld_u > LA_MAX_LD || in->ld_delta > LA_MAX_LD ||
@@ -89,7 +98,7 @@ int check_scan(const la_scan_inputs* in, long long rows, int D, int G, int n, in
 
 int check_ws(const void* ws, size_t have, size_t need)
 {
-    return need > 0 && (!ws || have < need || !aligned16(ws)) ? LA_ERR_WORKSPACE : LA_OK;
+    return need > 0 && (!ws || have < need || !aligned(ws, 16)) ? LA_ERR_WORKSPACE : LA_OK;
 }
 
 int check_conv(const void* x, long long ld_x, const float* weight, const float* bias,
@@ -99,7 +108,7 @@ int check_conv(const void* x, long long ld_x, const float* weight, const float* 
     if (W < 2 || W > 4) return LA_ERR_UNSUPPORTED;
     if (int st = check_types(in_t, out_t)) return st;
     if (!weight || (rows > 0 && !x)) return LA_ERR_INVALID_ARG;
-    if (!aligned(x, elem(in_t)) || !aligned16(weight) || !aligned16(bias))
+    if (!aligned(x, elem(in_t)) || !dense(weight, (long long)D * W, 4) || !dense(bias, D, 4))
         return LA_ERR_INVALID_ARG;
     if (rows > 1 && ld_x > LA_MAX_LD) return LA_ERR_UNSUPPORTED;
     return rows > 1 && ld_x < D ? LA_ERR_INVALID_ARG : LA_OK;
@@ -125,7 +134,9 @@ LA_API int la_selective_scan(const int* cu_seqlens, int num_seqs, const la_scan_
     int st = check_sequences(cu_seqlens, num_seqs, total, D, p.view);
     if (st != LA_OK || (st = check_scan(in, total, D, G, n, in_t, out_t)) != LA_OK) return st;
     if (total > 0 && !y) return LA_ERR_INVALID_ARG;
-    if (!aligned16(y) || !aligned16(state_in) || !aligned16(state_out)) return LA_ERR_INVALID_ARG;
+    const long long DN = (long long)D * n;
+    if (!dense(y, D, elem(out_t)) || !dense(state_in, DN, 4) || !dense(state_out, DN, 4))
+        return LA_ERR_INVALID_ARG;
     st = check_ws(workspace, ws_bytes, scan_workspace(false, G, D, total, n, num_seqs));
     if (st != LA_OK) return st;
     if (num_seqs == 0) return LA_OK;
@@ -146,7 +157,8 @@ LA_API int la_selective_scan_step(const la_scan_inputs* in, float* state, void* 
     int st = check_sequences(nullptr, B, B, D, p.view);
     if (st != LA_OK || (st = check_scan(in, B, D, G, n, in_t, out_t)) != LA_OK) return st;
     if (B == 0) return LA_OK;
-    if (!state || !y || !aligned16(state) || !aligned16(y)) return LA_ERR_INVALID_ARG;
+    if (!state || !y || !dense(state, (long long)D * n, 4) || !dense(y, D, elem(out_t)))
+        return LA_ERR_INVALID_ARG;
     p.in = *in;
     p.D = D;
     p.G = G;
@@ -172,10 +184,12 @@ LA_API int la_selective_scan_backward(const int* cu_seqlens, int num_seqs,
     if (total > 0 && !in->z != !out->dz) return LA_ERR_INVALID_ARG;
     if (!aligned(dy, elem(in_t)) || (total > 1 && ld_dy < D)) return LA_ERR_INVALID_ARG;
     if (total > 1 && ld_dy > LA_MAX_LD) return LA_ERR_UNSUPPORTED;
-    if (!aligned16(state_in) || !aligned16(dstate_out) || !aligned16(out->du) ||
-        !aligned16(out->ddelta) || !aligned16(out->dz) || !aligned16(out->dB) ||
-        !aligned16(out->dC) || !aligned16(out->dA) || !aligned16(out->dD) ||
-        !aligned16(out->ddelta_bias) || !aligned16(out->dstate_in))
+    const long long DN = (long long)D * n, GN = (long long)G * n;
+    const size_t e = elem(out_t);
+    if (!dense(state_in, DN, 4) || !dense(dstate_out, DN, 4) || !dense(out->du, D, e) ||
+        !dense(out->ddelta, D, e) || !dense(out->dz, D, e) || !dense(out->dB, GN, e) ||
+        !dense(out->dC, GN, e) || !dense(out->dA, DN, 4) || !dense(out->dD, D, 4) ||
+        !dense(out->ddelta_bias, D, 4) || !dense(out->dstate_in, DN, 4))
         return LA_ERR_INVALID_ARG;
     st = check_ws(workspace, ws_bytes, scan_workspace(true, G, D, total, n, num_seqs));
     if (st != LA_OK) return st;
@@ -200,7 +214,9 @@ LA_API int la_short_conv(const int* cu_seqlens, int num_seqs, const void* x, lon
     if (st != LA_OK || (st = check_conv(x, ld_x, weight, bias, total, D, W, in_t, out_t)) != LA_OK)
         return st;
     if (total > 0 && !y) return LA_ERR_INVALID_ARG;
-    if (!aligned16(y) || !aligned16(state_in) || !aligned16(state_out) ||
+    const long long rest = (long long)(W - 1) * D;  // of a state
+    if (!dense(y, D, elem(out_t)) || !dense(state_in, rest, elem(in_t)) ||
+        !dense(state_out, rest, elem(in_t)) ||
         (state_out && state_out == state_in))
         return LA_ERR_INVALID_ARG;
     if (num_seqs == 0) return LA_OK;
@@ -226,7 +242,9 @@ LA_API int la_short_conv_step(const void* x, long long ld_x, const float* weight
     if (st != LA_OK || (st = check_conv(x, ld_x, weight, bias, B, D, W, in_t, out_t)) != LA_OK)
         return st;
     if (B == 0) return LA_OK;
-    if (!state || !y || !aligned16(state) || !aligned16(y)) return LA_ERR_INVALID_ARG;
+    if (!state || !y || !dense(state, (long long)(W - 1) * D, elem(in_t)) ||
+        !dense(y, D, elem(out_t)))
+        return LA_ERR_INVALID_ARG;
     p.x = x;
     p.ld_x = ld_x;
     p.weight = weight;
@@ -255,8 +273,10 @@ LA_API int la_short_conv_backward(const int* cu_seqlens, int num_seqs, const voi
     if (!dweight || (total > 0 && (!dy || !dx))) return LA_ERR_INVALID_ARG;
     if (!aligned(dy, elem(in_t)) || (total > 1 && ld_dy < D)) return LA_ERR_INVALID_ARG;
     if (total > 1 && ld_dy > LA_MAX_LD) return LA_ERR_UNSUPPORTED;
-    if (!aligned16(state_in) || !aligned16(dstate_out) || !aligned16(dx) || !aligned16(dweight) ||
-        !aligned16(dbias) || !aligned16(dstate_in))
+    const long long rest = (long long)(W - 1) * D;  // of a state
+    if (!dense(state_in, rest, elem(in_t)) || !dense(dstate_out, rest, elem(in_t)) ||
+        !dense(dx, D, elem(out_t)) || !dense(dweight, (long long)D * W, 4) || !dense(dbias, D, 4) ||
+        !dense(dstate_in, rest, elem(out_t)))
         return LA_ERR_INVALID_ARG;
     if ((st = check_ws(workspace, ws_bytes, conv_backward_workspace(D, total, W))) != LA_OK)
         return st;
@@ -282,7 +302,8 @@ int check_norm(const void* x, const float* weight, const float* bias, long long 
     if (F > LA_MAX_NORM_FEATURES || rows > LA_MAX_TOKENS) return LA_ERR_UNSUPPORTED;
     if (int st = check_types(in_t, out_t)) return st;
     if (rows > 0 && (!x || !weight)) return LA_ERR_INVALID_ARG;
-    return aligned16(x) && aligned16(weight) && aligned16(bias) ? LA_OK : LA_ERR_INVALID_ARG;
+    return dense(x, F, elem(in_t)) && dense(weight, F, 4) && dense(bias, F, 4) ? LA_OK
+                                                                               : LA_ERR_INVALID_ARG;
 }
 
 }  // namespace
@@ -297,7 +318,7 @@ LA_API int la_layer_norm(const void* x, const float* weight, const float* bias, 
     if (!(eps >= 0.f) || eps > 3.0e38f) return LA_ERR_INVALID_ARG;  // also rejects NaN
     if (rows == 0) return LA_OK;
     if (!y || !mean != !rstd || (y == x && in_t != out_t)) return LA_ERR_INVALID_ARG;
-    if (!aligned16(y) || !aligned(mean, 4) || !aligned(rstd, 4)) return LA_ERR_INVALID_ARG;
+    if (!dense(y, F, elem(out_t)) || !aligned(mean, 4) || !aligned(rstd, 4)) return LA_ERR_INVALID_ARG;
     return status_of(launch_layer_norm(x, weight, bias, eps, y, mean, rstd, rows, F, in_t, out_t,
                                        stream_of(stream)));
 }
@@ -311,8 +332,8 @@ LA_API int la_layer_norm_backward(const void* dy, const void* x, const float* we
     int st = check_norm(x, weight, dbias, rows, F, in_t, out_t);
     if (st != LA_OK) return st;
     if (!dweight || (rows > 0 && (!dy || !mean || !rstd || !dx))) return LA_ERR_INVALID_ARG;
-    if (!aligned16(dy) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned16(dx) ||
-        !aligned16(dweight))
+    if (!dense(dy, F, elem(in_t)) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+        !dense(dx, F, elem(out_t)) || !dense(dweight, F, 4))
         return LA_ERR_INVALID_ARG;
     if ((st = check_ws(workspace, ws_bytes, norm_backward_workspace(rows, F))) != LA_OK) return st;
     return status_of(launch_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias,

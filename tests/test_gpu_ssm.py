@@ -725,3 +725,61 @@ def test_launch_counts():
     assert L.lib().la_short_conv_step(ctypes.c_void_p(0), D, w.data_ptr(), None, None, None, 1, D, 4, 1, 1, 1,
                                       None) == L.LA_ERR_INVALID_ARG
     assert L.la_last_launch_count() == 0
+
+
+def test_slices_of_stacked_tensors_of_odd_widths():
+    """Tensors that start inside a larger one (x[1:], a layer's weights in a stack
+    of them), where their width leaves them aligned to their elements only: the
+    bits of aligned copies."""
+    g = torch.Generator(device=DEV).manual_seed(0)
+
+    def inner(*shape, dtype=F32):
+        return torch.randn((2, *shape), generator=g, device=DEV).to(dtype)[1]
+
+    def both(fn, *args, **kw):
+        def flat(v):
+            vs = v.values() if isinstance(v, dict) else v if isinstance(v, tuple) else (v,)
+            return [t for t in vs if t is not None]
+
+        copy = lambda v: v.clone() if isinstance(v, torch.Tensor) else v  # noqa: E731
+        clones = [copy(a) for a in args], {k: copy(v) for k, v in kw.items()}
+        first, second = flat(fn(*args, **kw)), flat(fn(*clones[0], **clones[1]))
+        assert all(torch.equal(a, b) for a, b in zip(first, second, strict=True)), fn.__name__
+        # the states that a step advances in place
+        for a, b in zip(args, clones[0]):
+            assert not isinstance(a, torch.Tensor) or torch.equal(a, b), fn.__name__
+
+    offsets = set()
+    for dtype in (BF, F32):
+        for D, n, N in ((41, 5, 33), (42, 3, 700), (45, 6, 33)):
+            B = 1 if N > 100 else 3
+            tok = lambda: inner(B, N, D, dtype=dtype)  # noqa: E731,B023
+            bc = lambda: inner(B, N, 1, n, dtype=dtype)  # noqa: E731,B023
+            u, z, dy, A = tok(), tok(), tok(), inner(D, n)
+            A.copy_(-A.abs() - 0.1)
+            args = (u, tok(), A, bc(), bc(), inner(D), z, inner(D))
+            offsets.add(A.data_ptr() % 16)
+            both(L.selective_scan, *args, state_in=inner(B, D, n))
+            both(L.selective_scan_backward, dy, *args, state_in=inner(B, D, n), dstate_out=inner(B, D, n))
+            one = [a[:, 0].contiguous() if a.shape[:2] == (B, N) else a for a in args]
+            both(lambda s, *a: L.selective_scan_step(*a[:5], s, *a[5:]), inner(B, D, n), *one)
+        for D, W in ((41, 4), (42, 3), (44, 2)):
+            x, dy, w, b = inner(3, 50, D, dtype=dtype), inner(3, 50, D, dtype=dtype), inner(D, W), inner(D)
+            st, ds = inner(3, W - 1, D, dtype=dtype), inner(3, W - 1, D, dtype=dtype)
+            both(L.short_conv, x, w, b, state_in=st)
+            both(L.short_conv_backward, dy, x, w, b, state_in=st, dstate_out=ds)
+            both(lambda s, *a: L.short_conv_step(*a, s), st, x[:, 0].contiguous(), w, b)
+        for rows, F in ((3, 41), (5, 1031), (3, 5003), (1, 9001)):
+            x, dy, w, b = inner(rows, F, dtype=dtype), inner(rows, F, dtype=dtype), inner(F), inner(F)
+            offsets.add(x.data_ptr() % 16)
+            both(L.layer_norm, x, w, b)
+            _, mean, rstd = L.layer_norm(x, w, b)
+            both(L.layer_norm_backward, dy, x, w, mean, rstd)
+            # and as an output, in place
+            want, at = L.layer_norm(x, w, b)[0], inner(rows, F, dtype=dtype)
+            at.copy_(x)
+            s, t = torch.cuda.current_stream().cuda_stream, int(dtype == F32)
+            assert L.lib().la_layer_norm(at.data_ptr(), w.data_ptr(), b.data_ptr(), 1e-5, at.data_ptr(), None,
+                                         None, rows, F, t, t, s) == L.LA_OK
+            assert torch.equal(at, want)
+    assert any(o % 4 for o in offsets) and any(o % 8 for o in offsets)

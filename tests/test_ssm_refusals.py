@@ -225,3 +225,39 @@ def test_binding_refuses_norm_of_a_scalar(lib, monkeypatch):
         L.layer_norm(one, torch.zeros(1))
     with pytest.raises(ValueError, match="no dimension"):
         L.layer_norm_backward(one, one, torch.zeros(1), one, one)
+
+
+def test_slices_of_odd_widths_are_taken(lib):
+    """A slice x[1:] of an aligned tensor whose rows allow no vectors is aligned to
+    its elements only. None of these calls launches: they have no rows, or end at
+    the check of the workspace, behind the tensors'."""
+    x, o2, o4, o8 = P(X), P(X + 2), P(X + 4), P(X + 8)
+    norm = lambda **k: lib.la_layer_norm(*{**dict(x=x, w=x, b=x, e=1e-5, y=x, m=x, r=x, rows=0, F=5003, i=1, o=1, st=None), **k}.values())  # noqa: E731,E501
+    assert norm(x=o4, w=o4, b=o8) == L.LA_OK
+    assert norm(x=o2, i=0) == L.LA_OK
+    assert norm(x=o8, F=5002) == L.LA_OK
+    assert norm(x=o4, F=5002) == L.LA_ERR_INVALID_ARG
+    assert norm(w=P(X + 1)) == L.LA_ERR_INVALID_ARG
+    back = lambda **k: lib.la_layer_norm_backward(*{**dict(dy=x, x=x, w=x, m=x, r=x, dx=x, dw=x, db=x, rows=4, F=5003, i=1, o=1, ws=None, n=0, st=None), **k}.values())  # noqa: E731,E501
+    assert back(dy=o4, x=o4, w=o4, dx=o4, dw=o4, db=o4) == L.LA_ERR_WORKSPACE
+    assert back(dx=o8, F=5004) == L.LA_ERR_INVALID_ARG
+    odd = dict(total=1 << 16, D=127, n=5, ws=0)
+    assert _scan(lib, **odd, A=X + 4, delta_bias=X + 4, st=X + 4, out=X + 4, y=X + 2) == L.LA_ERR_WORKSPACE
+    assert _scan(lib, **odd, y=X + 2, ot=1) == L.LA_ERR_INVALID_ARG
+    assert _scan(lib, **{**odd, "n": 16}, st=X + 4) == L.LA_ERR_INVALID_ARG
+    assert _scan(lib, **{**odd, "D": 126}, y=X + 2) == L.LA_ERR_INVALID_ARG
+    o = X + 4
+    grads = L.SCAN_GRADS.pack(X + 2, X + 2, X + 2, X + 2, X + 2, o, o, o, o)
+    args = [_inputs(A=o, D=o, delta_bias=o), P(o), x, 128, P(o), grads, 64, 127, 1, 5, 0, 0, None, 0, None]
+    assert lib.la_selective_scan_backward(None, 2, *args) == L.LA_ERR_WORKSPACE
+    args[6 + 1] = 128  # a width of whole vectors
+    assert lib.la_selective_scan_backward(None, 2, *args) == L.LA_ERR_INVALID_ARG
+    none = dict(seqs=0, total=0)
+    assert _conv(lib, **none, D=13, W=3, w=X + 4, b=X + 4, y=X + 2, st=X + 8, out=X + 4) == L.LA_OK
+    assert _conv(lib, **none, D=13, W=3, st=X + 2) == L.LA_ERR_INVALID_ARG  # two rows of 13: 52 bytes
+    assert _conv(lib, **none, D=12, W=3, w=X + 4) == L.LA_ERR_INVALID_ARG
+    assert _conv(lib, **none, D=12, W=2, st=X + 8) == L.LA_OK
+    assert _conv(lib, **none, D=12, W=2, st=X + 4) == L.LA_ERR_INVALID_ARG
+    conv = lambda **k: lib.la_short_conv_backward(*{**dict(cu=None, s=2, dy=x, ldy=64, x=x, ld=64, w=x, b=x, si=None, so=None, dx=x, dw=x, db=x, ds=None, t=32, D=63, W=4, a=1, i=0, o=0, ws=None, n=0, st=None), **k}.values())  # noqa: E731,E501
+    assert conv(w=o8, b=o4, si=o2, so=o2, dx=o2, dw=o8, db=o4, ds=o2) == L.LA_ERR_INVALID_ARG  # weight: 63 * 16 bytes
+    assert conv(W=3, w=o4, b=o4, si=o4, so=o4, dx=o2, dw=o4, db=o4, ds=o4) == L.LA_ERR_WORKSPACE
