@@ -320,7 +320,9 @@ LA_API int la_backward(const void* dO, const void* q, const void* k, const void*
  *     dt     = softplus(delta[t][c] + delta_bias[c])   (without softplus: the sum itself)
  *     h_t[m] = exp(dt A[c][m]) h_{t-1}[m] + dt u[t][c] B[t][g][m]
  *     y[t][c] = ( sum_m C[t][g][m] h_t[m] + D[c] u[t][c] ) * z[t][c] sigmoid(z[t][c])
- * D and delta_bias may be NULL (0), z may be NULL (no gate).
+ * D and delta_bias may be NULL (0), z may be NULL (no gate). A softplus below
+ * 2^-126 (of less than -87.34) is 0. A = -inf forgets its state at every step dt of
+ * 3.7e-37 or more (a softplus of -83.8); a smaller one may keep some or all of it.
  *   u, delta, z  [tokens][D] (ld_u, ld_delta, ld_z), dtype in_t
  *   B, C         [tokens][G][n] (ld_b, ld_c; n contiguous, then G), dtype in_t
  *   A            [D][n] fp32, D and delta_bias [D] fp32
@@ -392,7 +394,10 @@ typedef struct {
  *   state_in    in  as in the forward call, or NULL
  *   dstate_out  in  [num_seqs][D][n] fp32, the gradient of state_out, or NULL for zeros
  *   out         du, ddelta, dz, dB, dC in dtype out_t
- *   workspace   at least la_workspace_bytes(LA_OP_SCAN_BACKWARD, ...) bytes
+ *   workspace   at least la_workspace_bytes(LA_OP_SCAN_BACKWARD, ...) bytes: for large
+ *               inputs about total * D * (n * (9/16 + K/32) + 9/16), K = 2 for n <= 8,
+ *               4 for n <= 16, 8 for n <= 32, else 16. That is several times the token
+ *               tensors: 3.1 GB for 32K tokens, D = 8192, n = 16, and 18.5 GB for n = 64
  */
 LA_API int la_selective_scan_backward(const int* cu_seqlens, int num_seqs,
                                       const la_scan_inputs* in, const float* state_in,

@@ -13,6 +13,12 @@
 // columns, which a CTA gathers in registers over the rows it walks and writes
 // as one partial row each; a second launch adds the partial rows. 16K rows of
 // 8192, bf16: 154-168 us, 4.8-5.2 TB/s.
+//
+// Beyond 8192 features 1024 threads leave 64 registers each: the ring spills (bf16
+// 220 to 228 bytes stored, fp32 32) and the backward too (272 in bf16, 384 in
+// fp32, which has no ring there; 400 to 420 without vectors). Widths that are no
+// whole vectors, 8 in bf16 or 4 in fp32, take single elements and no ring however
+// many rows there are.
 #include "ssm_scan.cuh"
 
 namespace la {
@@ -672,7 +678,7 @@ cudaError_t launch_ring(const void* x, const float* weight, const float* bias, f
     } while (0)
 #define LA_NORM_TYPES(SIZES)                                                                     \
     if (in_t == LA_F32) { if (F % 4 == 0) SIZES(float, float, 4); else SIZES(float, float, 1); } \
-    else if (dxvt == LA_F32) {                                                                  \
+    else if (out_t == LA_F32) {                                                                  \
         if (F % 8 == 0) SIZES(__nv_bfloat16, float, 8); else SIZES(__nv_bfloat16, float, 1);     \
     } else {                                                                                     \
         if (F % 8 == 0) SIZES(__nv_bfloat16, __nv_bfloat16, 8);                                  \
@@ -681,7 +687,7 @@ cudaError_t launch_ring(const void* x, const float* weight, const float* bias, f
 
 cudaError_t launch_layer_norm(const void* x, const float* weight, const float* bias, float eps,
                               void* y, float* mean, float* rstd, long long rows, int F, int in_t,
-                              int dxvt, cudaStream_t stream)
+                              int out_t, cudaStream_t stream)
 {
 #define LA_WARP(T, To, V, CH)                                                                    \
     norm_warp_kernel<T, To, V, CH><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(              \
@@ -738,7 +744,7 @@ cudaError_t launch_backward(const void* dy, const void* x, const float* weight, 
 cudaError_t launch_layer_norm_backward(const void* dy, const void* x, const float* weight,
                                        const float* mean, const float* rstd, void* dx,
                                        float* dweight, float* dbias, long long rows, int F,
-                                       int in_t, int dxvt, void* ws, cudaStream_t stream)
+                                       int in_t, int out_t, void* ws, cudaStream_t stream)
 {
     const int ctas = back_ctas(rows, F);
     float* dw = (float*)ws;

@@ -10,10 +10,12 @@
 // its incoming state.
 //
 // Measured, bf16, W = 4: 4 x 8K tokens of 8192 channels 191-203 us, 5.3-5.6 TB/s.
-// The backward of 2 x 8K takes 202-206 us, 3.9-4.0 TB/s: its arithmetic (about 27
-// instructions per element and thread, two of them on the special function
-// unit) sets the pace, not memory; two channels per thread, for more warps per
-// SM, took 250 us.
+// The backward of 2 x 8K takes 202-206 us, 3.9-4.0 TB/s. Neither memory (42% of
+// DRAM's peak) nor issue (50% of the cycles) is full: its 128 registers leave 14
+// warps per SM, whose latencies set the pace, over about 27 instructions per
+// element where the formula has 12 in pairs. Two channels per thread, for more
+// warps per SM, took 250 us. In fp32 four channels spill (W = 4 236 bytes stored,
+// W = 3 76).
 #include "ssm_scan.cuh"
 
 namespace la {

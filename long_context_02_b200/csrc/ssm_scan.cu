@@ -19,8 +19,12 @@
 // exponential exp(A sum dt) is the chunk's whole decay; the second launch
 // folds the chunks before its own, h <- exp(A sum dt_c) h + h_c, and scans
 // with outputs. That takes the exponentials twice, so it pays from about
-// three chunks on: 46K packed fp32 tokens of 1024 channels take 664 us, 287 in
-// the first launch and 387 in the second.
+// three chunks on: 46K packed fp32 tokens of 1024 channels take 664 us (under the
+// profiler, launch by launch, 4 for the table of chunks, 288 and 388), against
+// 385 for the exponentials of both walks. Scanning and serving threads share one
+// register budget, 80 with 256 servers and 96 with 512: the first launch spills
+// for n above 4 (60 to 84 bytes stored), the second with fp32 inputs, 256
+// servers and n up to 16 (132 to 156). What that costs has not been measured.
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -396,8 +400,10 @@ __global__ void __launch_bounds__(NT + SV, SV == 256 ? 2 : 1) scan_kernel(ScanAr
 // together. What depends on the channel alone is shared out: each of the
 // channel's K lanes makes dt, dt u and the gate of BB / K sequences, passes the
 // former on, and finishes the output of the same ones. 256 sequences of 8192
-// channels, 16 states: 61 us, 4.7 TB/s (every lane making every element 120 us,
-// with bounds checks on whole vectors 95 us).
+// channels, 16 states: 61-63 us, 4.5-4.7 TB/s (every lane making every element
+// 120 us, with bounds checks on whole vectors 95 us). It is latency that keeps it
+// from the 44 us of its bytes: a CTA takes one group of sequences, waits for all
+// its loads and has nothing on its way while it computes and stores.
 constexpr int BB = 4;
 
 // Four of B or C at p (the thread's first is m0 of n).

@@ -9,10 +9,12 @@
 //  2. combine: forward over the chunks, the state before each; backward over
 //     them, the gradient of the state after each (from dstate_out).
 //  3. main pass: the blocks of a chunk from the last to the first. The state
-//     before a block is its local part plus the decayed state before the chunk;
-//     a forward walk over the 8 tokens keeps their states in registers, a
-//     reverse walk carries the gradient. The exponentials are taken once per
-//     walk, three times in all.
+//     before a block is its local part plus the decayed state before the chunk.
+//     Half a block at a time, the second half first, a forward walk keeps the
+//     states of 4 tokens in registers and a reverse walk carries the gradient;
+//     the second half's states need a walk over the first half before. So the
+//     exponentials are taken 20 times per 8 tokens here, with the local pass 3.5
+//     times in all.
 //  4. reductions of dB and dC over the channel blocks and of dA, dD and
 //     ddelta_bias over the chunks, from partial sums in the workspace, in a
 //     fixed order.
@@ -21,12 +23,18 @@
 // the same path), would otherwise take longer than the exponentials.
 //
 // 2 x 4K tokens of 4096 channels, 16 states, bf16: 1,038 us (bytes alone 72 us;
-// the exponentials of three walks and the elementwise ones 400 us), of which
+// the exponentials of 3.5 walks and the elementwise ones 483 us), of which
 // the local pass 250, combine 25, the main pass 735, the sums 30. No single unit
 // bounds the main pass: its warps issue in 55% of the cycles, the special
 // function unit is busy in 39%, shared memory in half of them, and four CTAs per
 // SM instead of three gain nothing; fewer instructions do. One channel per
-// thread took 2,104 us in all.
+// thread took 2,104 us in all. For n up to 8 the main pass spills (fp32 124 bytes
+// stored, bf16 32), for n up to 16 with fp32 inputs too (16 to 20).
+//
+// The workspace is mostly the states before the blocks, total / 8 D n fp32, and
+// the partial sums of dB and dC, 2 cpg total G n fp32, where the channel blocks
+// per group, cpg, grow with n: 3.1 GB for 32K tokens of 8192 channels with 16
+// states, 18.5 GB with 64.
 #include <climits>
 
 #include "ssm_scan.cuh"
@@ -223,7 +231,7 @@ __device__ __forceinline__ f2 channel_pair(const float* v, int c, int c_end)
     return pack(v && c < c_end ? v[c] : 0.f, v && c + 1 < c_end ? v[c + 1] : 0.f);
 }
 
-// -A log2 e etc. of a thread's four states of two channels.
+// A log2 e of a thread's four states of two channels.
 __device__ __forceinline__ void load_decays(f2 (*A)[2], const BackArgs& a, int c, int c_end, int m0)
 {
 #pragma unroll

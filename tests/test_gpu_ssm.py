@@ -783,3 +783,27 @@ def test_slices_of_stacked_tensors_of_odd_widths():
                                          None, rows, F, t, t, s) == L.LA_OK
             assert torch.equal(at, want)
     assert any(o % 4 for o in offsets) and any(o % 8 for o in offsets)
+
+
+def test_scan_forgets_at_small_steps_where_a_is_infinite():
+    """From dt = 3.7e-37 on a state with A = -inf is gone after its next token,
+    without and with a softplus (of -83), packed, chunked and as a single token."""
+    D, n = 6, 4
+    g = torch.Generator(device=DEV).manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    A = -torch.rand((D, n), generator=g, device=DEV) - 0.1
+    A[2, 1] = A[4] = float("-inf")
+    gone = torch.isinf(A)
+    for N in (1, 5, 300):
+        for dt, softplus in ((3.8e-37, False), (-83.0, True)):
+            u, B, C, st = r(1, N, D), r(1, N, 1, n), r(1, N, 1, n), r(1, D, n)
+            delta = torch.full((1, N, D), dt, device=DEV)
+            y, out = L.selective_scan(u, delta, A, B, C, softplus=softplus, state_in=st)
+            # 1e-30: what 300 tokens of dt u B can bring
+            assert (out[0][gone].abs() < 1e-30).all() and torch.equal(out[0][~gone], st[0][~gone])
+            assert (y[0, :, 4].abs() < 1e-30).all()
+            if N == 1:
+                one = L.selective_scan_step(u[:, 0], delta[:, 0], A, B[:, 0], C[:, 0], st, softplus=softplus)
+                assert torch.equal(st, out)
+                # the four products of a channel, below 25 in all, are added in another order
+                assert ((one - y[:, 0]).abs() <= 6 * 2.0 ** -24 * 25).all()
